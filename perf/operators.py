@@ -203,7 +203,7 @@ def _norm_i8_plain(s):
     # products in 64 bits, where they are exact: the integers next to a rounding border come out the same everywhere
     p = h.double() * s["weight"].double()
     a = p.abs().amax(-1, keepdim=True)
-    q = torch.round(p * torch.where(a > 0, 127.0 / a, torch.zeros_like(a)))
+    q = torch.round(p * torch.where(a > 0, torch.full_like(a, 127.0) / a, torch.zeros_like(a)))
     scale = a.float() * rstd / 127.0
     return {"h": h, "values": q.float() * scale}
 
@@ -296,7 +296,7 @@ def exact(case, seed):
         step = y.abs().amax(1, keepdim=True) / 127.0
         p = h * w
         top = p.abs().amax(1, keepdim=True)
-        q = torch.where(top > 0, torch.round(p * (127.0 / top)), torch.zeros_like(p))
+        q = torch.where(top > 0, torch.round(p * (torch.full_like(top, 127.0) / top)), torch.zeros_like(p))
         return {"h": h, "values": q * step}
     gy = s["grad_out"].double()
     along = (gy * w * unit).sum(1, keepdim=True) / h.shape[1]
