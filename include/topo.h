@@ -336,6 +336,99 @@ tc_status tc_build_kernel_map_noalloc(const tc_grid_batch* src, const tc_grid_ba
                                       int32_t stride, int32_t transposed, int32_t* d_out, int64_t capacity,
                                       void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators on feature rows. A voxel of a batch is one row of a feature matrix,
+ * row j being voxel j of tc_enumerate_ijk; a kernel map's entries are rows of
+ * its source's features. Any other matrix with one row per token is taken alike.
+ *
+ * Conventions: matrices are row-major with unit channel stride; an input's
+ * `*_stride` is the distance between rows in elements (at least 0: a stride of
+ * 0 repeats one row), outputs without a stride are contiguous. No alignment
+ * beyond the element's own is required; rows that start on 16-byte boundaries
+ * take the wide loads. Nothing is allocated and nothing blocks: the calls may be
+ * captured into a HIP graph. An output may not overlap an input, except where
+ * said. A pointer whose array is empty may be NULL. Channels are 1 to 2^20. */
+typedef enum tc_dtype { TC_F32 = 0, TC_F16 = 1, TC_BF16 = 2 } tc_dtype;
+
+/* Root-mean-square norm of every row with the residual's addition (training form):
+ *   h = x + r, rounded to dtype; s = 1 / sqrt(mean(h^2) + eps); out = h s w, rounded to dtype.
+ * The norm is that of the rounded h. Sums and s are 32-bit floats.
+ *   d_x         dtype[n_rows][channels], x_stride.
+ *   d_residual  dtype[n_rows][channels], residual_stride, or NULL (h = x).
+ *   d_weight    weight_dtype[channels] (TC_F32, or dtype), or NULL (ones).
+ *   eps         finite, >= 0.
+ *   d_sum       dtype[n_rows][channels]: h, or NULL. With contiguous rows it may
+ *               be d_x or d_residual itself.
+ *   d_out       dtype[n_rows][channels].
+ *   d_rstd      float[n_rows]: s, or NULL. */
+tc_status tc_rms_norm(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
+                      const void* d_weight, int32_t weight_dtype, int64_t n_rows, int32_t channels, int32_t dtype,
+                      float eps, void* d_sum, void* d_out, float* d_rstd, void* stream);
+
+/* The same norm with an output in 8 bits and a scale for each row (serving form):
+ *   p = h w, a = max over the row of |p|; q = p * (127 / a) rounded to nearest even;
+ *   scale = a s / 127, so that q * scale stands for h s w.
+ * p is exact in 64 bits and the norm's factor s cancels out of q, so q is the same
+ * integer in any implementation that follows the line above in 64 bits.
+ * A row with a = 0 has q = 0 and scale = 0; a row with an infinity or NaN in p has
+ * q = 0 and scale = NaN. Other arguments as for tc_rms_norm.
+ *   d_q      int8[n_rows][channels], in [-127, 127].
+ *   d_scale  float[n_rows]. */
+tc_status tc_rms_norm_i8(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
+                         const void* d_weight, int32_t weight_dtype, int64_t n_rows, int32_t channels, int32_t dtype,
+                         float eps, void* d_sum, int8_t* d_q, float* d_scale, void* stream);
+
+/* Gradient of tc_rms_norm. With dy the gradient of out, dh that of h by its other
+ * uses (the residual stream) and g = dy w:
+ *   grad_x = s g - h s^3 mean(g h) + dh, rounded to dtype: the gradient of x, and of r alike;
+ *   grad_weight = sum over rows of dy h s, a 32-bit float sum in an order that
+ *   only n_rows and channels decide.
+ *   d_grad_out   dtype[n_rows][channels], grad_out_stride.
+ *   d_grad_sum   dh, dtype[n_rows][channels], grad_sum_stride, or NULL (zeros).
+ *   d_h          h as tc_rms_norm left it (x where there is no residual), h_stride.
+ *   d_rstd       float[n_rows]: s as tc_rms_norm left it.
+ *   d_grad_x     dtype[n_rows][channels], or NULL. With contiguous rows it may be
+ *                d_grad_sum itself.
+ *   d_grad_weight float[channels], or NULL (not both NULL). Zeros without rows.
+ *   d_workspace  tc_rms_norm_backward_workspace(n_rows, channels) bytes, 16-byte
+ *                aligned, read and written in stream order; may be NULL when
+ *                d_grad_weight is. */
+tc_status tc_rms_norm_backward(const void* d_grad_out, int64_t grad_out_stride, const void* d_grad_sum,
+                               int64_t grad_sum_stride, const void* d_h, int64_t h_stride, const void* d_weight,
+                               int32_t weight_dtype, const float* d_rstd, int64_t n_rows, int32_t channels,
+                               int32_t dtype, void* d_grad_x, float* d_grad_weight, void* d_workspace,
+                               int64_t workspace_bytes, void* stream);
+
+/* Bytes of d_workspace; 0 for arguments that tc_rms_norm_backward refuses. */
+int64_t tc_rms_norm_backward_workspace(int64_t n_rows, int32_t channels);
+
+/* Product of 8-bit rows with 8-bit weights, scales per row and per output channel:
+ *   out[m][n] = x_scale[m] * w_scale[n] * sum_c x[m][c] w[n][c] + bias[n], rounded to out_dtype.
+ * The sum is exact (int32); the rest is 32-bit float.
+ *   d_x        int8[n_rows][c_in], x_stride; d_x_scale float[n_rows].
+ *   d_w        int8[c_out][c_in], w_stride;  d_w_scale float[c_out].
+ *   d_bias     float[c_out], or NULL.
+ *   c_in       1 to 131071 (more could leave int32: TC_ERR_UNSUPPORTED).
+ *   d_out      out_dtype[n_rows][c_out], out_stride >= c_out elements. */
+tc_status tc_matmul_i8(const int8_t* d_x, int64_t x_stride, const float* d_x_scale, const int8_t* d_w,
+                       int64_t w_stride, const float* d_w_scale, const float* d_bias, int64_t n_rows, int32_t c_out,
+                       int32_t c_in, int32_t out_dtype, void* d_out, int64_t out_stride, void* stream);
+
+/* The same product over a kernel map: the convolution a map of tc_build_kernel_map
+ * stands for, with the rows in 8 bits:
+ *   out[j][n] = w_scale[n] * sum_t x_scale[i] * sum_c x[i][c] w[t][n][c] + bias[n], i = map[j][t],
+ * rounded to out_dtype; a tap whose entry lies outside [0, n_src) adds nothing.
+ * Sums over channels are exact (int32), the sum over taps is a 32-bit float sum
+ * in an order that only the sizes decide.
+ *   d_x       int8[n_src][c_in], x_stride; d_x_scale float[n_src].
+ *   d_map     int32[n_dst][taps], taps in [1, 512].
+ *   d_w       int8[taps][c_out][c_in], contiguous; d_w_scale float[c_out].
+ * n_src is at most INT32_MAX. Other arguments as for tc_matmul_i8. */
+tc_status tc_sparse_conv_i8(const int8_t* d_x, int64_t x_stride, const float* d_x_scale, int64_t n_src,
+                            const int32_t* d_map, int64_t n_dst, int32_t taps, const int8_t* d_w,
+                            const float* d_w_scale, const float* d_bias, int32_t c_out, int32_t c_in,
+                            int32_t out_dtype, void* d_out, int64_t out_stride, void* stream);
+
 /* Cached device memory: every call takes its scratch arrays (and the buffers
  * of intermediate batches) from blocks cached process-wide per device, stream
  * and allocator, and keeps them for the next call with the same key (reuse is

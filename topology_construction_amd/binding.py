@@ -4,7 +4,8 @@ Every step of the topology pass runs in the HIP library ``libtopo.so``; this
 module only converts torch tensors to device pointers, passes torch's current
 stream, supplies torch's caching allocator for the output buffers and wraps the
 results as torch tensor views. It never computes topology itself and raises
-when the library is missing.
+when the library is missing. The operators on feature rows (tc_rms_norm,
+tc_matmul_i8, tc_sparse_conv_i8, ...) take and return torch tensors directly.
 
 Function names follow the C ABI (tc_batch_from_ijk, tc_build_batched_topology,
 tc_enumerate_ijk, tc_batch_read_headers, ...).
@@ -30,6 +31,8 @@ ABI_SYMBOLS = [
     "tc_batch_voxel_total", "tc_enumerate_ijk", "tc_build_kernel_map", "tc_scratch_release", "tc_batch_free",
     "tc_debug_inject_flags", "tc_build_kernel_map_noalloc", "tc_profile_enable", "tc_profile_read",
     "tc_profile_disable", "tc_build_batched_topology_many", "tc_enumerate_ijk_many", "tc_debug_wide_loads",
+    "tc_rms_norm", "tc_rms_norm_i8", "tc_rms_norm_backward", "tc_rms_norm_backward_workspace", "tc_matmul_i8",
+    "tc_sparse_conv_i8",
 ]
 
 HEADER_DTYPE = np.dtype([
@@ -150,6 +153,19 @@ def load_library(path: str = LIB_PATH):
         lib.tc_profile_read.restype = ctypes.c_int
         lib.tc_profile_read.argtypes = [ctypes.c_char_p, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64)]
         lib.tc_profile_disable.restype = ctypes.c_int
+        f32 = ctypes.c_float
+        lib.tc_rms_norm.restype = ctypes.c_int
+        lib.tc_rms_norm.argtypes = [vp, i64, vp, i64, vp, i32, i64, i32, i32, f32, vp, vp, vp, vp]
+        lib.tc_rms_norm_i8.restype = ctypes.c_int
+        lib.tc_rms_norm_i8.argtypes = [vp, i64, vp, i64, vp, i32, i64, i32, i32, f32, vp, vp, vp, vp]
+        lib.tc_rms_norm_backward.restype = ctypes.c_int
+        lib.tc_rms_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, vp, i64, i32, i32, vp, vp, vp, i64, vp]
+        lib.tc_rms_norm_backward_workspace.restype = i64
+        lib.tc_rms_norm_backward_workspace.argtypes = [i64, i32]
+        lib.tc_matmul_i8.restype = ctypes.c_int
+        lib.tc_matmul_i8.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, i32, i32, i32, vp, i64, vp]
+        lib.tc_sparse_conv_i8.restype = ctypes.c_int
+        lib.tc_sparse_conv_i8.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, vp, vp, i32, i32, i32, vp, i64, vp]
         if lib.tc_abi_version() != 1:
             raise ImportError("libtopo.so ABI version mismatch")
         _lib = lib
@@ -496,6 +512,178 @@ def tc_build_kernel_map_noalloc(src: GridBatch, dst: GridBatch, kernel_size: int
         src.handle, dst.handle, int(kernel_size), int(stride), int(bool(transposed)),
         ctypes.c_void_p(out.data_ptr() if out.numel() else 0), int(out.numel()), _stream_handle(stream)))
     return out.view(-1)[:rows * kk].view(rows, kk)
+
+
+# -- operators on feature rows ------------------------------------------------
+_dtype_ids: dict = {}  # torch dtype -> tc_dtype
+
+
+def _dtype_id(dtype) -> int:
+    if not _dtype_ids:
+        import torch
+        _dtype_ids.update({torch.float32: 0, torch.float16: 1, torch.bfloat16: 2})
+    i = _dtype_ids.get(dtype)
+    if i is None:
+        raise TypeError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
+    return i
+
+
+def _matrix(t, name: str, dtype, rows=None, cols=None):
+    """A device matrix with unit channel stride (any row stride) as (pointer, row stride)."""
+    if not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a cuda {dtype} tensor")
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{'rows' if rows is None else rows}, "
+                         f"{'channels' if cols is None else cols}]")
+    stride, unit = t.stride()
+    if unit != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must have unit channel stride")
+    return t.data_ptr(), stride
+
+
+def _vector(t, name: str, dtype, n: int) -> int:
+    if not t.is_cuda or t.dtype != dtype:
+        raise TypeError(f"{name} must be a cuda {dtype} tensor")
+    if t.dim() != 1 or t.shape[0] != n or (t.stride(0) != 1 and n > 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n}")
+    return t.data_ptr()
+
+
+def _same_device(t, *others):
+    import torch
+    if not t.is_cuda:
+        raise TypeError("the tensors must be cuda tensors")
+    d = t.get_device()
+    if d != torch.cuda.current_device():
+        raise ValueError("the tensors are not on the current device")
+    for o in others:
+        if o is not None and o.get_device() != d:
+            raise ValueError("the tensors are on different devices")
+
+
+def _norm_inputs(x, weight, residual):
+    dt = _dtype_id(x.dtype)
+    _same_device(x, weight, residual)
+    px, sx = _matrix(x, "x", x.dtype)
+    rows, channels = x.shape
+    pr, sr = _matrix(residual, "residual", x.dtype, rows, channels) if residual is not None else (None, 0)
+    pw, wdt = None, dt
+    if weight is not None:
+        wdt = _dtype_id(weight.dtype)
+        pw = _vector(weight, "weight", weight.dtype, channels)
+    return px, sx, pr, sr, pw, wdt, rows, channels, dt
+
+
+def tc_rms_norm(x, weight=None, residual=None, eps: float = 1e-6, stream=None):
+    """Root-mean-square norm of rows: h = x + residual, s = 1 / sqrt(mean(h^2) + eps),
+    out = h * s * weight. Returns (out, h, rstd): h is x itself without a residual,
+    rstd float32 [rows] is s, kept for tc_rms_norm_backward."""
+    import torch
+    px, sx, pr, sr, pw, wdt, rows, channels, dt = _norm_inputs(x, weight, residual)
+    out = _empty_on(stream, (rows, channels), x.dtype)
+    h = _empty_on(stream, (rows, channels), x.dtype) if residual is not None else x
+    rstd = _empty_on(stream, (rows,), torch.float32)
+    _check(load_library().tc_rms_norm(px, sx, pr, sr, pw, wdt, rows, channels, dt, eps,
+                                      h.data_ptr() if residual is not None else None, out.data_ptr(), rstd.data_ptr(),
+                                      _stream_handle(stream)))
+    return out, h, rstd
+
+
+def tc_rms_norm_i8(x, weight=None, residual=None, eps: float = 1e-6, stream=None):
+    """The norm with an 8-bit output: (q int8 [rows, channels], scale float32 [rows], h),
+    q * scale standing for h * s * weight."""
+    import torch
+    px, sx, pr, sr, pw, wdt, rows, channels, dt = _norm_inputs(x, weight, residual)
+    q = _empty_on(stream, (rows, channels), torch.int8)
+    scale = _empty_on(stream, (rows,), torch.float32)
+    h = _empty_on(stream, (rows, channels), x.dtype) if residual is not None else x
+    _check(load_library().tc_rms_norm_i8(px, sx, pr, sr, pw, wdt, rows, channels, dt, eps,
+                                         h.data_ptr() if residual is not None else None, q.data_ptr(),
+                                         scale.data_ptr(), _stream_handle(stream)))
+    return q, scale, h
+
+
+def tc_rms_norm_backward(grad_out, h, weight, rstd, grad_h=None, stream=None):
+    """Gradient of tc_rms_norm from what it returned: (grad_x, grad_weight). grad_x is
+    the gradient of x and of the residual alike, `grad_h` (if given) that of h by its
+    other uses; grad_weight is float32 [channels], None without a weight."""
+    import torch
+    lib = load_library()
+    dt = _dtype_id(h.dtype)
+    _same_device(h, grad_out, weight, rstd, grad_h)
+    ph, sh = _matrix(h, "h", h.dtype)
+    rows, channels = h.shape
+    pg, sg = _matrix(grad_out, "grad_out", h.dtype, rows, channels)
+    pd, sd = _matrix(grad_h, "grad_h", h.dtype, rows, channels) if grad_h is not None else (None, 0)
+    pw, wdt, grad_weight, work, nbytes = None, dt, None, None, 0
+    if weight is not None:
+        wdt = _dtype_id(weight.dtype)
+        pw = _vector(weight, "weight", weight.dtype, channels)
+        grad_weight = _empty_on(stream, (channels,), torch.float32)
+        nbytes = lib.tc_rms_norm_backward_workspace(rows, channels)
+        work = _empty_on(stream, (max(nbytes, 1),), torch.uint8)
+    grad_x = _empty_on(stream, (rows, channels), h.dtype)
+    _check(lib.tc_rms_norm_backward(pg, sg, pd, sd, ph, sh, pw, wdt, _vector(rstd, "rstd", torch.float32, rows), rows,
+                                    channels, dt, grad_x.data_ptr(),
+                                    grad_weight.data_ptr() if grad_weight is not None else None,
+                                    work.data_ptr() if work is not None else None, nbytes, _stream_handle(stream)))
+    return grad_x, grad_weight
+
+
+def _product_out(out, rows, channels, out_dtype, stream):
+    if out is None:
+        out = _empty_on(stream, (rows, channels), out_dtype)
+        return out, out.data_ptr(), channels
+    ptr, stride = _matrix(out, "out", out.dtype, rows, channels)
+    if stride < channels and rows > 1:
+        raise ValueError("the rows of out overlap")
+    return out, ptr, max(stride, channels)
+
+
+def tc_matmul_i8(x, x_scale, w, w_scale, bias=None, out_dtype=None, out=None, stream=None):
+    """Product of int8 rows x [rows, c_in] with int8 weights w [c_out, c_in], float32
+    scales for each row and each output channel, float32 bias [c_out]: [rows, c_out]
+    of `out_dtype` (bfloat16 unless given), or into `out` (any row stride)."""
+    import torch
+    _same_device(x, x_scale, w, w_scale, bias, out)
+    px, sx = _matrix(x, "x", torch.int8)
+    rows, c_in = x.shape
+    pw, sw = _matrix(w, "w", torch.int8, None, c_in)
+    c_out = w.shape[0]
+    xs = _vector(x_scale, "x_scale", torch.float32, rows)
+    ws = _vector(w_scale, "w_scale", torch.float32, c_out)
+    pb = _vector(bias, "bias", torch.float32, c_out) if bias is not None else None
+    out, po, so = _product_out(out, rows, c_out, out_dtype or torch.bfloat16, stream)
+    _check(load_library().tc_matmul_i8(px, sx, xs, pw, sw, ws, pb, rows, c_out, c_in, _dtype_id(out.dtype), po, so,
+                                       _stream_handle(stream)))
+    return out
+
+
+def tc_sparse_conv_i8(x, x_scale, kmap, w, w_scale, bias=None, out_dtype=None, out=None, stream=None):
+    """Convolution of int8 rows x [n_src, c_in] over a kernel map [n_dst, taps] (as
+    tc_build_kernel_map returns it) with int8 weights w [taps, c_out, c_in]; scales,
+    bias and output as for tc_matmul_i8."""
+    import torch
+    _same_device(x, x_scale, kmap, w, w_scale, bias, out)
+    px, sx = _matrix(x, "x", torch.int8)
+    n_src, c_in = x.shape
+    if not kmap.is_cuda or kmap.dtype != torch.int32:
+        raise TypeError("kmap must be a cuda int32 tensor")
+    if kmap.dim() != 2 or not kmap.is_contiguous():
+        raise ValueError("kmap must be a contiguous [n_dst, taps] tensor")
+    n_dst, taps = kmap.shape
+    if not w.is_cuda or w.dtype != torch.int8:
+        raise TypeError("w must be a cuda int8 tensor")
+    if w.dim() != 3 or w.shape[0] != taps or w.shape[2] != c_in or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous [{taps}, c_out, {c_in}] tensor")
+    c_out = w.shape[1]
+    xs = _vector(x_scale, "x_scale", torch.float32, n_src)
+    ws = _vector(w_scale, "w_scale", torch.float32, c_out)
+    pb = _vector(bias, "bias", torch.float32, c_out) if bias is not None else None
+    out, po, so = _product_out(out, n_dst, c_out, out_dtype or torch.bfloat16, stream)
+    _check(load_library().tc_sparse_conv_i8(px, sx, xs, n_src, kmap.data_ptr(), n_dst, taps, w.data_ptr(), ws, pb,
+                                            c_out, c_in, _dtype_id(out.dtype), po, so, _stream_handle(stream)))
+    return out
 
 
 def tc_scratch_release():

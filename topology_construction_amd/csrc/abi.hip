@@ -304,6 +304,69 @@ tc_status op_passes(int32_t op, int32_t factor, std::vector<int>& passes, std::s
 
 }  // namespace tc
 
+// ------------------------------------------------------------------ arguments of the operators on feature rows
+namespace {
+
+constexpr int32_t kMaxChannels = 1 << 20;
+constexpr int32_t kMaxProductChannels = 131071;  // 128 * 128 * 131071 < 2^31
+
+void need(bool ok, const char* msg) {
+  if (!ok) throw tc::Error(TC_ERR_INVALID_ARG, msg);
+}
+bool is_dtype(int32_t d) { return d == TC_F32 || d == TC_F16 || d == TC_BF16; }
+
+void check_norm_shape(int64_t n_rows, int32_t channels, int32_t dtype, const void* weight, int32_t weight_dtype) {
+  need(n_rows >= 0, "n_rows is negative");
+  need(channels >= 1, "channels must be positive");
+  need(is_dtype(dtype), "unknown dtype");
+  need(!weight || weight_dtype == TC_F32 || weight_dtype == dtype, "weight_dtype must be TC_F32 or dtype");
+  if (channels > kMaxChannels) throw tc::Error(TC_ERR_UNSUPPORTED, "more than 2^20 channels");
+}
+
+void check_rows(const void* p, int64_t stride, int64_t n_rows, const char* name) {
+  if (!p && n_rows > 0) throw tc::Error(TC_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (stride < 0) throw tc::Error(TC_ERR_INVALID_ARG, std::string(name) + ": negative row stride");
+}
+
+tc::NormArgs norm_args(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
+                       const void* d_weight, int32_t weight_dtype, int64_t n_rows, int32_t channels, int32_t dtype,
+                       float eps, void* d_sum) {
+  check_norm_shape(n_rows, channels, dtype, d_weight, weight_dtype);
+  check_rows(d_x, x_stride, n_rows, "d_x");
+  if (d_residual) check_rows(d_residual, residual_stride, n_rows, "d_residual");
+  need(std::isfinite(eps) && eps >= 0.0f, "eps must be finite and not negative");
+  tc::NormArgs a{};
+  a.x = d_x;
+  a.x_stride = x_stride;
+  a.residual = d_residual;
+  a.residual_stride = residual_stride;
+  a.weight = d_weight;
+  a.weight_dtype = weight_dtype;
+  a.rows = n_rows;
+  a.channels = channels;
+  a.dtype = dtype;
+  a.eps = eps;
+  a.sum = d_sum;
+  return a;
+}
+
+void check_product(const tc::ProductArgs& a) {
+  need(a.rows >= 0 && a.n_src >= 0, "negative row count");
+  need(a.n >= 1 && a.k >= 1, "c_out and c_in must be positive");
+  need(is_dtype(a.out_dtype), "unknown out_dtype");
+  if (a.k > kMaxProductChannels) throw tc::Error(TC_ERR_UNSUPPORTED, "c_in above 131071: the sums could leave int32");
+  if (a.n > kMaxChannels) throw tc::Error(TC_ERR_UNSUPPORTED, "more than 2^20 output channels");
+  check_rows(a.x, a.x_stride, a.rows > 0 ? a.n_src : 0, "d_x");
+  need(a.x_scale || a.n_src == 0 || a.rows == 0, "d_x_scale is NULL");
+  need(a.out_stride >= a.n, "out_stride below c_out");
+  if (a.rows == 0) return;
+  need(a.w && a.w_scale, "d_w or d_w_scale is NULL");
+  need(a.w_stride >= 0, "d_w: negative row stride");
+  need(a.out != nullptr, "d_out is NULL");
+}
+
+}  // namespace
+
 extern "C" {
 
 int32_t tc_abi_version(void) { return TC_ABI_VERSION; }
@@ -741,6 +804,136 @@ tc_status tc_build_kernel_map_noalloc(const tc_grid_batch* src, const tc_grid_ba
                                               " bytes of scratch; the no-allocation entry point has " +
                                               std::to_string(cap) + " (use tc_build_kernel_map)");
     tc::kernel_map(src->view(), dst->view(), kernel_size, stride, transposed, d_out, need, s, scratch, cap);
+    return TC_OK;
+  });
+}
+
+// ------------------------------------------------------------------ operators on feature rows
+tc_status tc_rms_norm(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
+                      const void* d_weight, int32_t weight_dtype, int64_t n_rows, int32_t channels, int32_t dtype,
+                      float eps, void* d_sum, void* d_out, float* d_rstd, void* stream) {
+  return guarded([&]() {
+    tc::NormArgs a = norm_args(d_x, x_stride, d_residual, residual_stride, d_weight, weight_dtype, n_rows, channels,
+                               dtype, eps, d_sum);
+    need(d_out || n_rows == 0, "d_out is NULL");
+    a.out = d_out;
+    a.rstd = d_rstd;
+    tc::rms_norm(a, (hipStream_t)stream);
+    return TC_OK;
+  });
+}
+
+tc_status tc_rms_norm_i8(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
+                         const void* d_weight, int32_t weight_dtype, int64_t n_rows, int32_t channels, int32_t dtype,
+                         float eps, void* d_sum, int8_t* d_q, float* d_scale, void* stream) {
+  return guarded([&]() {
+    tc::NormArgs a = norm_args(d_x, x_stride, d_residual, residual_stride, d_weight, weight_dtype, n_rows, channels,
+                               dtype, eps, d_sum);
+    need((d_q && d_scale) || n_rows == 0, "d_q or d_scale is NULL");
+    a.q = d_q;
+    a.scale = d_scale;
+    tc::rms_norm(a, (hipStream_t)stream);
+    return TC_OK;
+  });
+}
+
+tc_status tc_rms_norm_backward(const void* d_grad_out, int64_t grad_out_stride, const void* d_grad_sum,
+                               int64_t grad_sum_stride, const void* d_h, int64_t h_stride, const void* d_weight,
+                               int32_t weight_dtype, const float* d_rstd, int64_t n_rows, int32_t channels,
+                               int32_t dtype, void* d_grad_x, float* d_grad_weight, void* d_workspace,
+                               int64_t workspace_bytes, void* stream) {
+  return guarded([&]() {
+    check_norm_shape(n_rows, channels, dtype, d_weight, weight_dtype);
+    check_rows(d_grad_out, grad_out_stride, n_rows, "d_grad_out");
+    if (d_grad_sum) check_rows(d_grad_sum, grad_sum_stride, n_rows, "d_grad_sum");
+    check_rows(d_h, h_stride, n_rows, "d_h");
+    need(d_rstd || n_rows == 0, "d_rstd is NULL");
+    need(d_grad_x || d_grad_weight || n_rows == 0, "d_grad_x and d_grad_weight are both NULL");
+    if (d_grad_weight) {
+      need(d_workspace != nullptr, "d_workspace is NULL");
+      need(workspace_bytes >= 0 && (size_t)workspace_bytes >= tc::rms_norm_grad_workspace(n_rows, channels),
+           "workspace_bytes below tc_rms_norm_backward_workspace");
+      need(((uintptr_t)d_workspace & 15) == 0, "d_workspace is not 16-byte aligned");
+    }
+    tc::NormGradArgs a{};
+    a.grad_out = d_grad_out;
+    a.grad_out_stride = grad_out_stride;
+    a.grad_sum = d_grad_sum;
+    a.grad_sum_stride = grad_sum_stride;
+    a.h = d_h;
+    a.h_stride = h_stride;
+    a.weight = d_weight;
+    a.weight_dtype = weight_dtype;
+    a.rstd = d_rstd;
+    a.rows = n_rows;
+    a.channels = channels;
+    a.dtype = dtype;
+    a.grad_x = d_grad_x;
+    a.grad_weight = d_grad_weight;
+    a.partial = static_cast<float*>(d_workspace);
+    tc::rms_norm_grad(a, (hipStream_t)stream);
+    return TC_OK;
+  });
+}
+
+int64_t tc_rms_norm_backward_workspace(int64_t n_rows, int32_t channels) {
+  if (n_rows < 0 || channels < 1 || channels > kMaxChannels) return 0;
+  return (int64_t)tc::rms_norm_grad_workspace(n_rows, channels);
+}
+
+tc_status tc_matmul_i8(const int8_t* d_x, int64_t x_stride, const float* d_x_scale, const int8_t* d_w,
+                       int64_t w_stride, const float* d_w_scale, const float* d_bias, int64_t n_rows, int32_t c_out,
+                       int32_t c_in, int32_t out_dtype, void* d_out, int64_t out_stride, void* stream) {
+  return guarded([&]() {
+    tc::ProductArgs a{};
+    a.x = d_x;
+    a.x_stride = x_stride;
+    a.x_scale = d_x_scale;
+    a.n_src = n_rows;
+    a.taps = 1;
+    a.w = d_w;
+    a.w_stride = w_stride;
+    a.w_scale = d_w_scale;
+    a.bias = d_bias;
+    a.rows = n_rows;
+    a.n = c_out;
+    a.k = c_in;
+    a.out_dtype = out_dtype;
+    a.out = d_out;
+    a.out_stride = out_stride;
+    check_product(a);
+    tc::product_i8(a, (hipStream_t)stream);
+    return TC_OK;
+  });
+}
+
+tc_status tc_sparse_conv_i8(const int8_t* d_x, int64_t x_stride, const float* d_x_scale, int64_t n_src,
+                            const int32_t* d_map, int64_t n_dst, int32_t taps, const int8_t* d_w,
+                            const float* d_w_scale, const float* d_bias, int32_t c_out, int32_t c_in,
+                            int32_t out_dtype, void* d_out, int64_t out_stride, void* stream) {
+  return guarded([&]() {
+    need(taps >= 1 && taps <= 512, "taps must be in [1, 512]");
+    if (n_src > (int64_t)INT32_MAX) throw tc::Error(TC_ERR_UNSUPPORTED, "source row indices exceed int32");
+    need(d_map || n_dst <= 0, "d_map is NULL");
+    tc::ProductArgs a{};
+    a.x = d_x;
+    a.x_stride = x_stride;
+    a.x_scale = d_x_scale;
+    a.n_src = n_src;
+    a.map = d_map;
+    a.taps = taps;
+    a.w = d_w;
+    a.w_stride = c_in;
+    a.w_scale = d_w_scale;
+    a.bias = d_bias;
+    a.rows = n_dst;
+    a.n = c_out;
+    a.k = c_in;
+    a.out_dtype = out_dtype;
+    a.out = d_out;
+    a.out_stride = out_stride;
+    check_product(a);
+    tc::product_i8(a, (hipStream_t)stream);
     return TC_OK;
   });
 }

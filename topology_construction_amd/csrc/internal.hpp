@@ -478,4 +478,63 @@ tc_grid_batch* build_pass(const tc_grid_batch* src, int op, const OutAlloc& oa,
 // a flag index outside [0, n_keep) sets the internal-error bit in *flags.
 void mask_leaves(const tc_grid_batch* src, const uint8_t* keep, i64 n_keep, u64* out_mask, int32_t* flags,
                  hipStream_t s);
+// ------------------------------------------------------------------ operators on feature rows (norm.hip, product.hip)
+struct NormArgs {
+  const void* x;
+  i64 x_stride;
+  const void* residual;  // nullptr: none
+  i64 residual_stride;
+  const void* weight;  // nullptr: ones
+  int weight_dtype;
+  i64 rows;
+  int channels;
+  int dtype;
+  float eps;
+  void* sum;     // nullptr: not wanted
+  void* out;     // training form
+  float* rstd;   // training form, nullptr: not wanted
+  int8_t* q;     // 8-bit form
+  float* scale;  // 8-bit form
+};
+void rms_norm(const NormArgs& a, hipStream_t s);
+
+struct NormGradArgs {
+  const void* grad_out;
+  i64 grad_out_stride;
+  const void* grad_sum;  // nullptr: none
+  i64 grad_sum_stride;
+  const void* h;
+  i64 h_stride;
+  const void* weight;  // nullptr: ones
+  int weight_dtype;
+  const float* rstd;
+  i64 rows;
+  int channels;
+  int dtype;
+  void* grad_x;        // nullptr: not wanted
+  float* grad_weight;  // nullptr: not wanted
+  float* partial;      // rms_norm_grad_workspace bytes, when grad_weight is wanted
+};
+size_t rms_norm_grad_workspace(i64 rows, int channels);
+void rms_norm_grad(const NormGradArgs& a, hipStream_t s);
+
+struct ProductArgs {
+  const int8_t* x;
+  i64 x_stride;
+  const float* x_scale;
+  i64 n_src;           // rows of x
+  const int32_t* map;  // [rows][taps], nullptr: row j reads x row j (taps = 1)
+  int taps;
+  const int8_t* w;  // [taps][n][w_stride]
+  i64 w_stride;
+  const float* w_scale;
+  const float* bias;  // nullptr: none
+  i64 rows;           // output rows
+  int n, k;           // output and input channels
+  int out_dtype;
+  void* out;
+  i64 out_stride;
+};
+void product_i8(const ProductArgs& a, hipStream_t s);
+
 }  // namespace tc
