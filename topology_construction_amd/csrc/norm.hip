@@ -5,7 +5,9 @@
 //
 // h is rounded to the rows' type once and the norm is the norm of that rounded
 // h, so the gradient taken from the stored h is the gradient of what was
-// computed. The mean is a float sum of float squares.
+// computed. The mean is a float sum of float squares. Memory bounds all of it:
+// every kernel reads a row once, holds it in registers over its reductions and
+// writes once.
 #include "rows.hpp"
 
 namespace tc {
@@ -13,7 +15,6 @@ namespace tc {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kNormRows = kNormThreads / kWave;  // one wave per row
 
 __device__ __forceinline__ float weight_at(const void* w, int dt, int c) {
   if (!w) return 1.0f;
@@ -22,72 +23,341 @@ __device__ __forceinline__ float weight_at(const void* w, int dt, int c) {
   return to_f32(static_cast<const bf16*>(w)[c]);
 }
 
-// One wave per row, one element per lane and step. The second pass reads h
-// where the first one stored it (the same lane's elements), else x and r again.
+// 16 bytes of a row, from any address.
 template <typename T>
+struct Vec {
+  static constexpr int kN = 16 / sizeof(T);
+  T v[kN];
+  __device__ __forceinline__ void load(const T* p) { __builtin_memcpy(v, p, 16); }
+  __device__ __forceinline__ void store(T* p) const { __builtin_memcpy(p, v, 16); }
+};
+
+// A group of L threads holds one row, N vectors a thread (vector g + j L for thread
+// g). A row that is no whole number of vectors has its last one moved back to end
+// the row: `skip` of its elements belong to the vector before as well, are written
+// twice with the same value, and are left out of the sums.
+template <typename T, int L, int N>
+struct RowPlace {
+  int c[N];     // first element, -1: none
+  int skip[N];
+  bool ragged;
+  __device__ __forceinline__ RowPlace(int channels) {
+    constexpr int V = Vec<T>::kN;
+    ragged = channels % V != 0;
+    const int g = threadIdx.x % L;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int at = (g + j * L) * V, from = min(at, channels - V);
+      c[j] = at < channels ? from : -1;
+      skip[j] = at - from;
+    }
+  }
+};
+
+// Sums over the L threads of a group, L a power of two up to a wave, or a workgroup of
+// four waves. Every thread gets the sum, in an order that only L decides.
+struct GroupScratch {
+  double d[2][4];
+  float f[2][4];
+};
+
+template <int L>
+__device__ __forceinline__ float group_sum(float v, GroupScratch& s, int turn) {
+  v = lanes_reduce<(L < kWave ? L : kWave)>(v, [](float a, float b) { return a + b; });
+  if constexpr (L > kWave) {
+    if ((threadIdx.x & (kWave - 1)) == 0) s.f[turn][threadIdx.x / kWave] = v;
+    __syncthreads();
+    v = (s.f[turn][0] + s.f[turn][1]) + (s.f[turn][2] + s.f[turn][3]);
+  }
+  return v;
+}
+
+// As group_sum, with the largest `top` beside the sum.
+template <int L>
+__device__ __forceinline__ void group_sum_max(float& v, double& top, GroupScratch& s, int turn) {
+  constexpr int W = L < kWave ? L : kWave;
+  v = lanes_reduce<W>(v, [](float a, float b) { return a + b; });
+  top = lanes_reduce<W>(top, [](double a, double b) { return fmax(a, b); });
+  if constexpr (L > kWave) {
+    if ((threadIdx.x & (kWave - 1)) == 0) {
+      s.f[turn][threadIdx.x / kWave] = v;
+      s.d[turn][threadIdx.x / kWave] = top;
+    }
+    __syncthreads();
+    v = (s.f[turn][0] + s.f[turn][1]) + (s.f[turn][2] + s.f[turn][3]);
+    top = fmax(fmax(s.d[turn][0], s.d[turn][1]), fmax(s.d[turn][2], s.d[turn][3]));
+  }
+}
+
+// |h w| in 64 bits, where it is exact; infinite for an infinity or NaN.
+__device__ __forceinline__ double magnitude(double p) {
+  p = fabs(p);
+  return p < INFINITY ? p : INFINITY;
+}
+
+// The factor of the row's 8-bit values, and its scale.
+__device__ __forceinline__ double row_factor(double top, float rstd, float& scale) {
+  const bool finite = top < INFINITY, some = top > 0.0;
+  scale = finite ? (some ? (float)top * rstd / 127.0f : 0.0f) : NAN;
+  return finite && some ? 127.0 / top : 0.0;
+}
+
+// p * factor, rounded to 64 bits, then to the nearest integer, ties to even: adding
+// 1.5 * 2^52 leaves it in the low bits. One fused operation would skip the first rounding.
+__device__ __forceinline__ int8_t nearest_i8(double p, double factor) {
+#pragma clang fp contract(off)
+  const double q = p * factor;
+  return (int8_t)__double2loint(q + 6755399441055744.0);
+}
+
+// The row stays in registers between the reductions and the outputs. h is stored
+// only after a reduction over the row, when all of x and r is read: it may go over either.
+template <typename T, int L, int N, bool kI8>
+__global__ void __launch_bounds__(kNormThreads) k_rms_norm(NormArgs a) {
+  constexpr int V = Vec<T>::kN;
+  __shared__ GroupScratch s_red;
+  const RowPlace<T, L, N> at(a.channels);
+  float w[N][V];
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[j][e] = at.c[j] >= 0 ? weight_at(a.weight, a.weight_dtype, at.c[j] + e) : 0.0f;
+  int turn = 0;
+  for (i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L; row < a.rows;
+       row += (i64)gridDim.x * (kNormThreads / L), turn ^= 1) {
+    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+    Vec<T> h[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (at.c[j] >= 0) h[j].load(x + at.c[j]);
+    if (a.residual) {
+      const T* r = static_cast<const T*>(a.residual) + row * a.residual_stride;
+      Vec<T> v[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (at.c[j] >= 0) v[j].load(r + at.c[j]);
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) h[j].v[e] = from_f32<T>(to_f32(h[j].v[e]) + to_f32(v[j].v[e]));
+    }
+    float ss = 0.0f;
+    double top = 0.0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (at.c[j] < 0) continue;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float f = to_f32(h[j].v[e]);
+        if (!at.ragged || e >= at.skip[j]) ss += f * f;
+        if constexpr (kI8) top = fmax(top, magnitude((double)f * (double)w[j][e]));
+      }
+    }
+    if constexpr (kI8) group_sum_max<L>(ss, top, s_red, turn);
+    else ss = group_sum<L>(ss, s_red, turn);
+    const float rstd = 1.0f / sqrtf(ss / (float)a.channels + a.eps);
+    const bool first = threadIdx.x % L == 0;
+    if (a.sum) {
+      T* sum = static_cast<T*>(a.sum) + row * a.channels;
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (at.c[j] >= 0) h[j].store(sum + at.c[j]);
+    }
+    if constexpr (kI8) {
+      float scale;
+      const double to_q = row_factor(top, rstd, scale);
+      if (first) a.scale[row] = scale;
+      int8_t* q = a.q + row * a.channels;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (at.c[j] < 0) continue;
+        int8_t b[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          b[e] = to_q > 0.0 ? nearest_i8((double)to_f32(h[j].v[e]) * (double)w[j][e], to_q) : 0;
+        __builtin_memcpy(q + at.c[j], b, V);
+      }
+    } else {
+      if (a.rstd && first) a.rstd[row] = rstd;
+      T* out = static_cast<T*>(a.out) + row * a.channels;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (at.c[j] < 0) continue;
+        Vec<T> o;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o.v[e] = from_f32<T>(to_f32(h[j].v[e]) * rstd * w[j][e]);
+        o.store(out + at.c[j]);
+      }
+    }
+  }
+}
+
+// dx = s g - h s^3 mean(g h) + dh with g = dy w, and this workgroup's part of
+// dw = sum over rows of dy h s: each thread adds up its channels over its rows in
+// registers, the workgroup's groups are joined once at the end.
+template <typename T, int L, int N, bool kWeight>
+__global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad(NormGradArgs a) {
+  constexpr int V = Vec<T>::kN;
+  __shared__ GroupScratch s_red;
+  const RowPlace<T, L, N> at(a.channels);
+  float w[N][V], dw[N][V];
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      w[j][e] = at.c[j] >= 0 ? weight_at(a.weight, a.weight_dtype, at.c[j] + e) : 0.0f;
+      dw[j][e] = 0.0f;
+    }
+  int turn = 0;
+  for (i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L; row < a.rows;
+       row += (i64)gridDim.x * (kNormThreads / L), turn ^= 1) {
+    const T* pdy = static_cast<const T*>(a.grad_out) + row * a.grad_out_stride;
+    const T* ph = static_cast<const T*>(a.h) + row * a.h_stride;
+    Vec<T> dy[N], h[N], dh[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (at.c[j] < 0) continue;
+      dy[j].load(pdy + at.c[j]);
+      h[j].load(ph + at.c[j]);
+    }
+    if (a.grad_sum) {
+      const T* pdh = static_cast<const T*>(a.grad_sum) + row * a.grad_sum_stride;
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (at.c[j] >= 0) dh[j].load(pdh + at.c[j]);
+    }
+    const float rstd = a.rstd[row];
+    float dot = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (at.c[j] < 0) continue;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float y = to_f32(dy[j].v[e]), f = to_f32(h[j].v[e]);
+        if (!at.ragged || e >= at.skip[j]) dot += y * w[j][e] * f;
+        if constexpr (kWeight) dw[j][e] += y * f * rstd;
+      }
+    }
+    dot = group_sum<L>(dot, s_red, turn);
+    if (!a.grad_x) continue;
+    const float k = rstd * rstd * rstd * (dot / (float)a.channels);
+    T* dx = static_cast<T*>(a.grad_x) + row * a.channels;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      if (at.c[j] < 0) continue;
+      Vec<T> o;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float v = rstd * (to_f32(dy[j].v[e]) * w[j][e]) - to_f32(h[j].v[e]) * k;
+        o.v[e] = from_f32<T>(a.grad_sum ? v + to_f32(dh[j].v[e]) : v);
+      }
+      o.store(dx + at.c[j]);
+    }
+  }
+  if constexpr (kWeight) {
+    float* part = a.partial + (i64)blockIdx.x * a.channels;
+    if constexpr (L > kWave) {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (at.c[j] >= 0) part[at.c[j] + e] = dw[j][e];
+    } else {
+      constexpr int kWaves = kNormThreads / kWave;
+      __shared__ float s_dw[kWaves][L * N * V];
+      const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float v = dw[j][e];
+#pragma unroll
+          for (int d = L; d < kWave; d <<= 1) v += __shfl_xor(v, d, kWave);
+          if (lane < L) s_dw[wave][(j * L + lane) * V + e] = v;
+        }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        // slot i of the row's vectors, as this thread's RowPlace has it where the thread is below L
+        for (int i = threadIdx.x; i < L * V; i += kNormThreads) {
+          const int vec = j * L + i / V, first = vec * V;
+          if (first >= a.channels) continue;
+          float v = s_dw[0][j * L * V + i];
+#pragma unroll
+          for (int k = 1; k < kWaves; ++k) v += s_dw[k][j * L * V + i];
+          part[min(first, a.channels - V) + i % V] = v;
+        }
+      }
+    }
+  }
+}
+
+// Rows of fewer channels than a vector has (L = 1: one thread a row), or of more
+// than a workgroup's registers hold (L = a workgroup, the row read twice).
+template <typename T, int L>
 __global__ void __launch_bounds__(kNormThreads) k_rms_norm_any(NormArgs a) {
-  const int lane = threadIdx.x & (kWave - 1);
-  for (i64 row = (i64)blockIdx.x * kNormRows + threadIdx.x / kWave; row < a.rows; row += (i64)gridDim.x * kNormRows) {
+  __shared__ GroupScratch s_red;
+  const int g = threadIdx.x % L;
+  int turn = 0;
+  for (i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L; row < a.rows;
+       row += (i64)gridDim.x * (kNormThreads / L), turn ^= 1) {
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
     const T* r = a.residual ? static_cast<const T*>(a.residual) + row * a.residual_stride : nullptr;
     T* sum = a.sum ? static_cast<T*>(a.sum) + row * a.channels : nullptr;
     float ss = 0.0f;
     double top = 0.0;
-    for (int c = lane; c < a.channels; c += kWave) {
+    for (int c = g; c < a.channels; c += L) {
       const T h = r ? from_f32<T>(to_f32(x[c]) + to_f32(r[c])) : x[c];
       if (sum) sum[c] = h;
       const float f = to_f32(h);
       ss += f * f;
-      if (a.q) {
-        // h w is exact in 64 bits; an infinity or NaN makes `top` infinite
-        const double p = fabs((double)f * (double)weight_at(a.weight, a.weight_dtype, c));
-        top = p < INFINITY ? fmax(top, p) : INFINITY;
-      }
+      if (a.q) top = fmax(top, magnitude((double)f * (double)weight_at(a.weight, a.weight_dtype, c)));
     }
-    ss = wave_sum_f32(ss);
+    group_sum_max<L>(ss, top, s_red, turn);
     const float rstd = 1.0f / sqrtf(ss / (float)a.channels + a.eps);
-    if (a.rstd && lane == 0) a.rstd[row] = rstd;
+    if (a.rstd && g == 0) a.rstd[row] = rstd;
     double to_q = 0.0;
     if (a.q) {
-      top = wave_max_f64(top);
-      const bool finite = top < INFINITY;
-      to_q = finite && top > 0.0 ? 127.0 / top : 0.0;
-      if (lane == 0) a.scale[row] = finite ? (top > 0.0 ? (float)top * rstd / 127.0f : 0.0f) : NAN;
+      float scale;
+      to_q = row_factor(top, rstd, scale);
+      if (g == 0) a.scale[row] = scale;
     }
-    for (int c = lane; c < a.channels; c += kWave) {
+    // h where this thread stored it, else x and r again
+    for (int c = g; c < a.channels; c += L) {
       const T h = sum ? sum[c] : (r ? from_f32<T>(to_f32(x[c]) + to_f32(r[c])) : x[c]);
       const float f = to_f32(h), w = weight_at(a.weight, a.weight_dtype, c);
       if (a.out) static_cast<T*>(a.out)[row * a.channels + c] = from_f32<T>(f * rstd * w);
-      if (a.q) a.q[row * a.channels + c] = to_q > 0.0 ? (int8_t)(int)rint((double)f * (double)w * to_q) : 0;
+      if (a.q) a.q[row * a.channels + c] = to_q > 0.0 ? nearest_i8((double)f * (double)w, to_q) : 0;
     }
   }
 }
 
-// dx = s g - h s^3 mean(g h) + dh with g = dy w; one wave per row.
-template <typename T>
+template <typename T, int L>
 __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad_any(NormGradArgs a) {
-  const int lane = threadIdx.x & (kWave - 1);
-  for (i64 row = (i64)blockIdx.x * kNormRows + threadIdx.x / kWave; row < a.rows; row += (i64)gridDim.x * kNormRows) {
+  __shared__ GroupScratch s_red;
+  const int g = threadIdx.x % L;
+  int turn = 0;
+  for (i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L; row < a.rows;
+       row += (i64)gridDim.x * (kNormThreads / L), turn ^= 1) {
     const T* dy = static_cast<const T*>(a.grad_out) + row * a.grad_out_stride;
     const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
     const T* dh = a.grad_sum ? static_cast<const T*>(a.grad_sum) + row * a.grad_sum_stride : nullptr;
     const float rstd = a.rstd[row];
     float dot = 0.0f;
-    for (int c = lane; c < a.channels; c += kWave)
+    for (int c = g; c < a.channels; c += L)
       dot += to_f32(dy[c]) * weight_at(a.weight, a.weight_dtype, c) * to_f32(h[c]);
-    dot = wave_sum_f32(dot);
+    dot = group_sum<L>(dot, s_red, turn);
     const float k = rstd * rstd * rstd * (dot / (float)a.channels);
-    for (int c = lane; c < a.channels; c += kWave) {
-      const float g = to_f32(dy[c]) * weight_at(a.weight, a.weight_dtype, c);
-      const float v = rstd * g - to_f32(h[c]) * k + (dh ? to_f32(dh[c]) : 0.0f);
-      static_cast<T*>(a.grad_x)[row * a.channels + c] = from_f32<T>(v);
+    for (int c = g; c < a.channels; c += L) {
+      const float gy = to_f32(dy[c]) * weight_at(a.weight, a.weight_dtype, c);
+      const float v = rstd * gy - to_f32(h[c]) * k;
+      static_cast<T*>(a.grad_x)[row * a.channels + c] = from_f32<T>(dh ? v + to_f32(dh[c]) : v);
     }
   }
 }
 
-// dw = sum over rows of dy h s, in two steps with a fixed order: block (column
-// group, part) adds a contiguous range of rows, then one thread per channel
-// adds the parts.
+// The weight gradient's parts for the rows of k_rms_norm_grad_any: block (column
+// group, part) adds a contiguous range of rows.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad_part(NormGradArgs a, int parts, i64 rows_per_part) {
   const int groups = (a.channels + kNormThreads - 1) / kNormThreads;
@@ -103,47 +373,116 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad_part(NormGradArg
   a.partial[(i64)part * a.channels + c] = acc;
 }
 
-__global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad_sum(const float* partial, int parts, int channels,
-                                                                    float* out) {
-  const int c = blockIdx.x * kNormThreads + threadIdx.x;
-  if (c >= channels) return;
+// dw: the sum of the parts, 32 channels by 32 slices of the parts a workgroup.
+constexpr int kSumChannels = 32, kSumSlices = 32;
+__global__ void __launch_bounds__(kSumChannels* kSumSlices)
+    k_rms_norm_grad_sum(const float* partial, int parts, int channels, float* out) {
+  __shared__ float s_part[kSumSlices][kSumChannels];
+  const int cl = threadIdx.x % kSumChannels, slice = threadIdx.x / kSumChannels;
+  const int c = blockIdx.x * kSumChannels + cl;
   float acc = 0.0f;
-  for (int p = 0; p < parts; ++p) acc += partial[(i64)p * channels + c];
-  out[c] = acc;
+  if (c < channels) {
+#pragma unroll 8
+    for (int p = slice; p < parts; p += kSumSlices) acc += partial[(i64)p * channels + c];
+  }
+  s_part[slice][cl] = acc;
+  __syncthreads();
+  if (slice == 0 && c < channels) {
+#pragma unroll
+    for (int k = 1; k < kSumSlices; ++k) acc += s_part[k][cl];
+    out[c] = acc;
+  }
 }
 
-// Parts of the weight gradient's sum over rows.
-int grad_parts(i64 rows) { return (int)std::max<i64>(1, std::min<i64>(256, ceil_div(rows, 64))); }
+// Workgroups whose parts of the weight gradient are joined at the end: enough to
+// have memory busy, while the parts stay small next to the rows.
+constexpr int kGradParts = 1024, kGradPartsWide = 512;
+int grad_parts(i64 rows, int channels) {
+  return (int)std::max<i64>(1, std::min<i64>(rows, channels <= 512 ? kGradParts : kGradPartsWide));
+}
+
+// Calls f<L, N> with the place of rows of `vectors` 16-byte vectors: the fewest
+// lanes that hold the row, up to four vectors a lane in one wave, then a workgroup.
+// False where a workgroup's registers do not hold the row.
+template <typename F>
+bool with_place(i64 vectors, F&& f) {
+  using std::integral_constant;
+  auto go = [&](auto l, auto n) { f(l, n); return true; };
+#define TC_PLACE(L, N) go(integral_constant<int, L>(), integral_constant<int, N>())
+  if (vectors <= 1) return TC_PLACE(1, 1);
+  if (vectors <= 2) return TC_PLACE(2, 1);
+  if (vectors <= 4) return TC_PLACE(4, 1);
+  if (vectors <= 8) return TC_PLACE(8, 1);
+  if (vectors <= 16) return TC_PLACE(16, 1);
+  if (vectors <= 32) return TC_PLACE(32, 1);
+  if (vectors <= 64) return TC_PLACE(64, 1);
+  if (vectors <= 128) return TC_PLACE(64, 2);
+  if (vectors <= 256) return TC_PLACE(256, 1);
+  if (vectors <= 512) return TC_PLACE(256, 2);
+  if (vectors <= 1024) return TC_PLACE(256, 4);
+  if (vectors <= 2048) return TC_PLACE(256, 8);
+#undef TC_PLACE
+  return false;
+}
 
 }  // namespace
 
 void rms_norm(const NormArgs& a, hipStream_t s) {
   if (a.rows == 0) return;
-  const i64 blocks = std::min<i64>(ceil_div(a.rows, kNormRows), (i64)device_cu_count() * 64);
+  const i64 most = (i64)device_cu_count() * 8;  // workgroups that fill the card; each takes its rows in turn
   with_dtype(a.dtype, [&](auto t) {
     using T = decltype(t);
-    launch("k_rms_norm_any", k_rms_norm_any<T>, blocks, kNormThreads, s, a);
+    constexpr int V = Vec<T>::kN;
+    auto blocks = [&](int rows) { return std::min<i64>(ceil_div(a.rows, rows), most); };
+    if (a.channels < V) return launch("k_rms_norm_any", k_rms_norm_any<T, 1>, blocks(kNormThreads), kNormThreads, s, a);
+    const bool held = with_place(ceil_div(a.channels, V), [&](auto l, auto n) {
+      constexpr int L = decltype(l)::value, N = decltype(n)::value;
+      if (a.q) launch("k_rms_norm", k_rms_norm<T, L, N, true>, blocks(kNormThreads / L), kNormThreads, s, a);
+      else launch("k_rms_norm", k_rms_norm<T, L, N, false>, blocks(kNormThreads / L), kNormThreads, s, a);
+    });
+    if (!held) launch("k_rms_norm_any", k_rms_norm_any<T, kNormThreads>, blocks(1), kNormThreads, s, a);
   });
 }
 
 size_t rms_norm_grad_workspace(i64 rows, int channels) {
-  return sizeof(float) * (size_t)grad_parts(rows) * (size_t)channels;
+  return sizeof(float) * (size_t)grad_parts(rows, channels) * (size_t)channels;
 }
 
 void rms_norm_grad(const NormGradArgs& a, hipStream_t s) {
   with_dtype(a.dtype, [&](auto t) {
     using T = decltype(t);
-    if (a.grad_x && a.rows)
-      launch("k_rms_norm_grad_any", k_rms_norm_grad_any<T>,
-             std::min<i64>(ceil_div(a.rows, kNormRows), (i64)device_cu_count() * 64), kNormThreads, s, a);
-    if (a.grad_weight) {
-      const int parts = grad_parts(a.rows);
-      const i64 groups = ceil_div(a.channels, kNormThreads);
-      launch("k_rms_norm_grad_part", k_rms_norm_grad_part<T>, groups * parts, kNormThreads, s, a, parts,
-             ceil_div(a.rows, parts));
-      launch("k_rms_norm_grad_sum", k_rms_norm_grad_sum, groups, kNormThreads, s, (const float*)a.partial, parts,
-             a.channels, a.grad_weight);
+    constexpr int V = Vec<T>::kN;
+    const i64 most = (i64)device_cu_count() * 8;
+    int parts = grad_parts(a.rows, a.channels);
+    bool held = false;
+    if (a.channels >= V && a.rows > 0)
+      held = with_place(ceil_div(a.channels, V), [&](auto l, auto n) {
+        constexpr int L = decltype(l)::value, N = decltype(n)::value;
+        const i64 groups = ceil_div(a.rows, kNormThreads / L);
+        if (a.grad_weight) {
+          parts = (int)std::min<i64>(parts, groups);
+          launch("k_rms_norm_grad", k_rms_norm_grad<T, L, N, true>, parts, kNormThreads, s, a);
+        } else {
+          launch("k_rms_norm_grad", k_rms_norm_grad<T, L, N, false>, std::min(groups, most), kNormThreads, s, a);
+        }
+      });
+    if (!held) {
+      const bool narrow = a.channels < V;
+      if (a.grad_x && a.rows) {
+        if (narrow)
+          launch("k_rms_norm_grad_any", k_rms_norm_grad_any<T, 1>,
+                 std::min(ceil_div(a.rows, kNormThreads), most), kNormThreads, s, a);
+        else
+          launch("k_rms_norm_grad_any", k_rms_norm_grad_any<T, kNormThreads>, std::min(a.rows, most), kNormThreads, s,
+                 a);
+      }
+      if (a.grad_weight)
+        launch("k_rms_norm_grad_part", k_rms_norm_grad_part<T>, ceil_div(a.channels, kNormThreads) * parts,
+               kNormThreads, s, a, parts, ceil_div(a.rows, parts));
     }
+    if (a.grad_weight)
+      launch("k_rms_norm_grad_sum", k_rms_norm_grad_sum, ceil_div(a.channels, kSumChannels), kSumChannels * kSumSlices,
+             s, (const float*)a.partial, parts, a.channels, a.grad_weight);
   });
 }
 

@@ -22,14 +22,27 @@ __device__ __forceinline__ T from_f32(float v) {
   return (T)v;
 }
 
-__device__ __forceinline__ float wave_sum_f32(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, kWave);
-  return v;
+// v of another lane: its partner in groups of 2, 4, 8, 16 (mirrored within 8 and 16) by
+// DPP, without LDS.
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), kCtrl, 0xf, 0xf, true));
 }
-__device__ __forceinline__ double wave_max_f64(double v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v = fmax(v, __shfl_xor(v, d, kWave));
+template <int kCtrl>
+__device__ __forceinline__ double dpp(double v) {
+  return __hiloint2double(__builtin_amdgcn_mov_dpp(__double2hiint(v), kCtrl, 0xf, 0xf, true),
+                          __builtin_amdgcn_mov_dpp(__double2loint(v), kCtrl, 0xf, 0xf, true));
+}
+
+// f over each group of L lanes (a power of two), the same result in every lane of the group.
+template <int L, typename V, typename F>
+__device__ __forceinline__ V lanes_reduce(V v, F&& f) {
+  if constexpr (L >= 2) v = f(v, dpp<0xb1>(v));    // lane ^ 1
+  if constexpr (L >= 4) v = f(v, dpp<0x4e>(v));    // lane ^ 2
+  if constexpr (L >= 8) v = f(v, dpp<0x141>(v));   // mirrored within 8
+  if constexpr (L >= 16) v = f(v, dpp<0x140>(v));  // mirrored within 16
+  if constexpr (L >= 32) v = f(v, __shfl_xor(v, 16, kWave));
+  if constexpr (L >= 64) v = f(v, __shfl_xor(v, 32, kWave));
   return v;
 }
 
