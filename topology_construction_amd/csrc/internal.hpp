@@ -535,6 +535,7 @@ struct ProductArgs {
   void* out;
   i64 out_stride;
 };
-void product_i8(const ProductArgs& a, hipStream_t s);
+void product_i8(const ProductArgs& a, hipStream_t s);  // also over a map
+void conv_i8(const ProductArgs& a, hipStream_t s);     // over a map, with rows
 
 }  // namespace tc

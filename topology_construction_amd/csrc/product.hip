@@ -1,108 +1,15 @@
-// Product of 8-bit feature rows with 8-bit weights, and the same product over
-// a kernel map (a sparse convolution).
+// Product of 8-bit feature rows with 8-bit weights.
 //
-//   out[j][n] = ws[n] * sum_t xs[i] * (sum_c x[i][c] * w[t][n][c]) + bias[n],  i = map[j][t]
+//   out[m][n] = xs[m] * ws[n] * (sum_c x[m][c] * w[n][c]) + bias[n]
 //
-// The inner sum is exact (int32 accumulators of the matrix instructions); the
-// sum over taps, whose rows have scales of their own, is a float sum in the
-// order of the taps.
-#include "rows.hpp"
+// The sum is exact (int32 accumulators of the matrix instructions).
+#include "int8.hpp"
 
 namespace tc {
 
 namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-
-constexpr int kTile = 64;       // output rows and channels of a workgroup
-constexpr int kStep = 64;       // input channels of one matrix instruction
-constexpr int kLdsRow = kStep + 16;  // bytes between rows in LDS
-
-// 16 bytes at row + c (c a multiple of 16), zeros from k on.
-__device__ __forceinline__ v4i load_16(const int8_t* row, int c, int k) {
-  union {
-    int8_t b[16];
-    v4i v;
-  } u;
-  u.v = v4i{0, 0, 0, 0};
-  if (row) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (c + i < k) u.b[i] = row[c + i];
-  }
-  return u.v;
-}
-
-// One workgroup of four waves per 64 x 64 output tile. The weights are the
-// matrix instruction's row operand and the feature rows its column operand, so
-// a lane holds four consecutive output channels of one output row.
-template <typename T>
-__global__ void __launch_bounds__(256) k_product_any(ProductArgs a) {
-  __shared__ __align__(16) int8_t s_x[kTile * kLdsRow];
-  __shared__ __align__(16) int8_t s_w[kTile * kLdsRow];
-  __shared__ float s_scale[kTile];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int tiles_n = (a.n + kTile - 1) / kTile;
-  const i64 row0 = (i64)(blockIdx.x / tiles_n) * kTile;
-  const int n0 = (blockIdx.x % tiles_n) * kTile;
-  const int lr = tid >> 2, lc = (tid & 3) * 16;  // this thread's row and bytes of both LDS tiles
-
-  v4f acc[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) acc[t] = v4f{0, 0, 0, 0};
-  for (int tap = 0; tap < a.taps; ++tap) {
-    i64 src = row0 + lr;
-    bool have = src < a.rows;
-    if (a.map) src = have ? (i64)a.map[src * a.taps + tap] : -1;
-    have = have && src >= 0 && src < a.n_src;
-    const int8_t* xrow = have ? a.x + src * a.x_stride : nullptr;
-    const int8_t* wrow = n0 + lr < a.n ? a.w + ((i64)tap * a.n + n0 + lr) * a.w_stride : nullptr;
-    if (lc == 0) s_scale[lr] = have ? a.x_scale[src] : 0.0f;
-    v4i dot[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) dot[t] = v4i{0, 0, 0, 0};
-    for (int c = 0; c < a.k; c += kStep) {
-      const v4i xv = load_16(xrow, c + lc, a.k), wv = load_16(wrow, c + lc, a.k);
-      __syncthreads();
-      *reinterpret_cast<v4i*>(s_x + lr * kLdsRow + lc) = xv;
-      *reinterpret_cast<v4i*>(s_w + lr * kLdsRow + lc) = wv;
-      __syncthreads();
-      const v4i xo = *reinterpret_cast<const v4i*>(s_x + (wave * 16 + (lane & 15)) * kLdsRow + (lane >> 4) * 16);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const v4i wo = *reinterpret_cast<const v4i*>(s_w + (t * 16 + (lane & 15)) * kLdsRow + (lane >> 4) * 16);
-        dot[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wo, xo, dot[t], 0, 0, 0);
-      }
-    }
-    if (a.k == 0) __syncthreads();
-    const float xs = s_scale[wave * 16 + (lane & 15)];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[t][i] += xs * (float)dot[t][i];
-    __syncthreads();  // the next tap rewrites the scales
-  }
-  const i64 row = row0 + wave * 16 + (lane & 15);
-  if (row >= a.rows) return;
-  T* out = static_cast<T*>(a.out) + row * a.out_stride;
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = n0 + t * 16 + (lane >> 4) * 4 + i;
-      if (n < a.n) out[n] = from_f32<T>(acc[t][i] * a.w_scale[n] + (a.bias ? a.bias[n] : 0.0f));
-    }
-}
-
 // ------------------------------------------------------------------ plain product, many tiles
-
-// Tile t of `total` for this workgroup. Workgroups go to the 8 XCDs in turn, each with
-// an L2 of its own: an XCD gets one contiguous range of tiles.
-__device__ __forceinline__ i64 xcd_tile(i64 total) {
-  const i64 b = blockIdx.x, q = total / 8, r = total % 8, x = b % 8;
-  return x * q + min(x, r) + b / 8;
-}
 
 // The tile of output rows and of output channels: runs of `kGroup` row tiles
 // take all channel tiles before the next run, so that tiles in flight together
@@ -115,67 +22,9 @@ __device__ __forceinline__ void tile_place(i64 tile, i64 tiles_m, int tiles_n, i
   tn = at / size;
 }
 
-// 16 consecutive output channels of one row from n on: dot * (row scale * channel scale) + bias.
-template <typename T>
-__device__ __forceinline__ void store_16(const ProductArgs& a, i64 row, int n, const float v[16], bool wide) {
-  T* out = static_cast<T*>(a.out) + row * a.out_stride + n;
-  T r[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = from_f32<T>(v[i]);
-  if (wide && n + 16 <= a.n) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(r) / 16; ++i)
-      reinterpret_cast<v4i*>(out)[i] = reinterpret_cast<const v4i*>(r)[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (n + i < a.n) out[i] = r[i];
-  }
-}
-
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  static_assert(N < 64, "vmcnt has 6 bits");
-  // vmcnt = N, the other counters left alone
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
-}
-
-// LDS keeps a row's 64 bytes of a step in four slots of 16. A wave reads 16 rows
-// of the same chunk at once; the chunk's slot depends on the row so that
-// neighbours in such a read fall into different banks.
-__device__ __forceinline__ int x_key(int row) { return (row >> 1) & 3; }
 // Row r of the weights' tile t is channel (r / 4) * 16 + t * 4 + r % 4 of a wave's 64, so
 // that a lane's results of four tiles are 16 consecutive channels.
 __device__ __forceinline__ int w_key(int row) { return ((row >> 1) & 1) | ((row >> 3) & 2); }
-
-// 16 bytes at row + c, from any address; zeros from k on (c a multiple of 16, k > 0).
-__device__ __forceinline__ v4i load_16_tail(const int8_t* row, int c, int k) {
-  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
-  u64x2 v{0, 0};
-  if (k >= 16) {  // the 16 bytes that end the row, or are before its end, moved down
-    const int from = min(c, k - 16), by = min(c - from, 16) * 8;
-    __builtin_memcpy(&v, row + from, 16);
-    const unsigned long long lo = by >= 64 ? v[1] : v[0], hi = by >= 64 ? 0 : v[1];
-    const int left = by & 63;
-    v[0] = by >= 128 ? 0 : (lo >> left) | (hi << 1 << (63 - left));
-    v[1] = hi >> left;
-  } else if (c == 0) {
-    for (int i = 0; i < k; ++i) v[i >> 3] |= (unsigned long long)(uint8_t)row[i] << (8 * (i & 7));
-  }
-  return __builtin_bit_cast(v4i, v);
-}
-
-// A buffer of at most 2^31 - 1 bytes from `base` on, for loads by 32-bit offsets.
-typedef __amdgpu_buffer_rsrc_t Buffer;
-constexpr unsigned kOutside = 0x80000000u;  // an offset out of every buffer's range: such a lane loads zeros
-__device__ __forceinline__ Buffer buffer_at(const int8_t* base) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(base), 0, 0x7fffffff, 0x00027000);
-}
-
-// 16 bytes per lane from the buffer into LDS at `to` + 16 * lane.
-__device__ __forceinline__ void load_to_lds(Buffer from, unsigned lane_at, unsigned at, int8_t* to) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void*)to, 16, lane_at, at, 0, 0);
-}
 
 // BM x BN outputs per workgroup, (BM / WM) * (BN / 64) waves of WM x 64 each, in
 // steps of 64 input channels. kDirect: rows and chunks on 16-byte boundaries go
@@ -192,7 +41,7 @@ __global__ void __launch_bounds__((BM / WM) * (BN / 64) * 64)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   i64 tm;
   int tn;
-  tile_place(xcd_tile(tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
+  tile_place(xcd_block(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
   const i64 row0 = tm * BM;
   const int n0 = tn * BN;
 
@@ -255,7 +104,7 @@ __global__ void __launch_bounds__((BM / WM) * (BN / 64) * 64)
 #pragma unroll
     for (int j = 0; j < kRows; ++j)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) dot[j][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[t], x[j], dot[j][t], 0, 0, 0);
+      for (int t = 0; t < 4; ++t) dot[j][t] = product_16(w[t], x[j], dot[j][t]);
     // reads two row groups ahead of the products
     __builtin_amdgcn_sched_group_barrier(0x100, kRows > 2 ? 6 : 4 + kRows, 0);
 #pragma unroll
@@ -265,14 +114,6 @@ __global__ void __launch_bounds__((BM / WM) * (BN / 64) * 64)
     }
     __builtin_amdgcn_sched_group_barrier(0x008, kRows > 2 ? 8 : 4 * kRows, 0);
   };
-  // every wave has its part of the step in LDS, and has read the step before
-  auto meet = [&]() {
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  };
-
   if constexpr (kDirect) {
 #pragma unroll
     for (int s = 0; s < kBufs - 1; ++s)
@@ -324,7 +165,7 @@ __global__ void __launch_bounds__((BM / WM) * (BN / 64) * 64)
     float v[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = xs * (float)dot[j][i >> 2][i & 3] * ws[i] + b[i];
-    store_16<T>(a, row, n, v, wide);
+    store_run<T, 16>(a, row, n, v, wide);
   }
 }
 
@@ -361,7 +202,7 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_product_few(ProductArgs a) {
 #pragma unroll
     for (int j = 0; j < kRows; ++j)
 #pragma unroll
-      for (int t = 0; t < kCols; ++t) dot[j][t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[t], x[j], dot[j][t], 0, 0, 0);
+      for (int t = 0; t < kCols; ++t) dot[j][t] = product_16(w[t], x[j], dot[j][t]);
   };
   auto load = [&](const int8_t* row, int c) {
     v4i v;
@@ -470,11 +311,8 @@ void plain_product(const ProductArgs& a, hipStream_t s) {
 
 void product_i8(const ProductArgs& a, hipStream_t s) {
   if (a.rows == 0 || a.n == 0) return;
-  with_dtype(a.out_dtype, [&](auto t) {
-    using T = decltype(t);
-    if (!a.map) return plain_product<T>(a, s);
-    launch("k_product_any", k_product_any<T>, ceil_div(a.rows, kTile) * ceil_div(a.n, kTile), 256, s, a);
-  });
+  if (a.map) return conv_i8(a, s);
+  with_dtype(a.out_dtype, [&](auto t) { plain_product<decltype(t)>(a, s); });
 }
 
 }  // namespace tc
