@@ -15,20 +15,18 @@ namespace {
 constexpr int kConvWaves = 4;
 
 // The row of an output tile's weights that row r of the matrix instruction t is, such
-// that a lane's results of consecutive t are consecutive output channels (16 of them;
-// with fewer than four instructions, 4 kCols).
+// that a lane's results of two instructions are 8 consecutive output channels.
 template <int kCols>
 __device__ __forceinline__ constexpr int weight_row(int t, int r) {
-  if (kCols >= 4) return (t >> 2) * 64 + (r >> 2) * 16 + (t & 3) * 4 + (r & 3);
-  return (r >> 2) * 4 * kCols + t * 4 + (r & 3);
+  if (kCols == 1) return r;
+  return (t >> 1) * 32 + (r >> 2) * 8 + (t & 1) * 4 + (r & 3);
 }
 // The LDS slot key of such a row: a function of r alone that differs between the
 // rows one read takes together, two by two.
 template <int kCols>
 __device__ __forceinline__ constexpr int weight_key(int row) {
-  if (kCols >= 4) return ((row >> 1) & 1) | ((row >> 3) & 2);
-  if (kCols == 2) return ((row >> 1) & 1) | ((row >> 2) & 2);
-  return (row >> 1) & 3;
+  if (kCols == 1) return (row >> 1) & 3;
+  return ((row >> 1) & 1) | ((row >> 2) & 2);
 }
 
 // 16 bytes of a row of k >= 16 channels for the chunk at c: the chunk, or the
@@ -80,14 +78,23 @@ struct Channels {
 //
 // Order of the rows: a tap is absent for most rows of a surface's map, and a group
 // of 16 skips the taps that none of its rows has. The tile's rows are sorted by the
-// Gray rank of their masks, so that rows of like masks share a group; group g goes to wave g % 4.
+// Gray rank of their masks, so that rows of like masks share a group (16 shells of
+// resolution 64, 39% of the entries there: 75% of the groups' taps in the rows' own order,
+// 64% sorted; a transposed 2x2x2: 70%, 16%); group g goes to wave g % 4.
 //
 // A stage is one tap and 64 kSteps input channels (kWide: the rows have more than that, a tap
 // takes several stages, and its integer sums are kept across them). Its weights are
 // shared by the waves, two stages of them in LDS. Its rows are gathered by each wave into
-// LDS of its own, in 16 rows x 64 bytes a load, and read from there as matrix operands
-// before the next stage's are asked for. kDirect: rows and weights on 16-byte boundaries go
-// straight into LDS, otherwise through registers, from any address.
+// LDS of its own, in 16 rows x 64 bytes a load (a lane's 16 bytes of a row of its own, as the
+// matrix operand has them, would cost a load three times the time), and read from there as
+// operands before the next stage's are asked for. kDirect: rows and weights on 16-byte
+// boundaries go straight into LDS, otherwise through registers, from any address.
+//
+// 116k rows, 27 taps, 128 -> 128: 69 us, 1.6 us a stage beside 15 for order and stores. Matrix
+// units (0.85 us a stage), LDS and gathers each take about half a stage: what is left
+// is that two workgroups a CU overlap them no better. Sharing the rows among waves that split
+// the channels (balanced skips, but three branches for every 64 products) took 81 us, all
+// groups without branches 78.
 template <int kRows, int kCols, int kSteps, bool kDirect, bool kWide>
 __global__ void __launch_bounds__(kConvWaves * 64, kWide ? 1 : 2) k_conv_tile(ProductArgs a, int tiles_n) {
   constexpr int BM = kConvWaves * kRows * 16, BN = kCols * 16;
@@ -106,11 +113,24 @@ __global__ void __launch_bounds__(kConvWaves * 64, kWide ? 1 : 2) k_conv_tile(Pr
   // the order of the tile's rows; at most 32 taps, evenly spread, decide it
   if (tid < BM) {
     uint32_t mask = 0;
-    if (row0 + tid < a.rows) {
-      const int32_t* m = a.map + (row0 + tid) * taps;
+    const int32_t* m = a.map + min(row0 + tid, a.rows - 1) * taps;
+    const auto has = [&](int e) { return (uint32_t)((uint32_t)e < (uint32_t)a.n_src); };
+    if (taps >= 4 && taps <= 32) {  // all loads under way together
+      v4i e[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i * 4 < taps) __builtin_memcpy(&e[i], m + min(i * 4, taps - 4), 16);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i * 4 < taps)
+          mask |= (has(e[i][0]) | has(e[i][1]) << 1 | has(e[i][2]) << 2 | has(e[i][3]) << 3) << min(i * 4, taps - 4);
+    } else {
       const int every = (taps + 31) / 32;
-      for (int t = 0, b = 0; t < taps; t += every, ++b) mask |= (uint32_t)((uint32_t)m[t] < (uint32_t)a.n_src) << b;
+#pragma unroll 8
+      for (int b = 0; b < 32; ++b)
+        if (b * every < taps) mask |= has(m[b * every]) << b;
     }
+    if (row0 + tid >= a.rows) mask = 0;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) mask ^= mask >> d;
     mask <<= taps < 32 ? 32 - taps : 0;
@@ -120,6 +140,7 @@ __global__ void __launch_bounds__(kConvWaves * 64, kWide ? 1 : 2) k_conv_tile(Pr
   if (tid < BM) {
     const uint32_t mine = s_key[tid];
     int rank = 0;
+#pragma unroll 8
     for (int i = 0; i < BM; i += 4) {
       const uint4 o = *reinterpret_cast<const uint4*>(s_key + i);
       rank += (o.x < mine) + (o.y < mine) + (o.z < mine) + (o.w < mine);
@@ -152,22 +173,18 @@ __global__ void __launch_bounds__(kConvWaves * 64, kWide ? 1 : 2) k_conv_tile(Pr
   const Buffer xb = buffer_at(a.x);
   v4i x_held[kDirect ? 1 : kRowLoads], w_held[kDirect ? 1 : kWeightLoads];
 
-  int entry = -1;      // the stage's map entry of this lane's row, -1: none
-  float scale = 0.0f;  // and its scale
-  unsigned long long have = 0;
-  auto take_entry = [&](int tap) {
+  // the map entry of this lane's row at a tap (taps in turn), -1: none
+  auto entry_at = [&](int tap) {
     if (tap > 0 && (tap & 3) == 0) {
       entries = entries_ahead;
       entries_ahead = four_entries(tap + 4);
     }
     const int at = tap - (taps >= 4 ? min(tap & ~3, taps - 4) : 0);
     const int e = at == 0 ? entries[0] : at == 1 ? entries[1] : at == 2 ? entries[2] : entries[3];
-    entry = live && (uint32_t)e < (uint32_t)a.n_src ? e : -1;
-    have = __ballot(entry >= 0);
-    scale = entry >= 0 ? a.x_scale[entry] : 0.0f;
+    return live && (uint32_t)e < (uint32_t)a.n_src ? e : -1;
   };
   auto group_has = [&](unsigned long long h, int j) { return (h >> (16 * j) & 0xffff) != 0; };
-  auto ask = [&](int tap, int c0, int buffer) {
+  auto ask = [&](int tap, int c0, int buffer, unsigned long long have, const unsigned (&src)[kRows]) {
     // weights
     const int8_t* wt = a.w + ((i64)tap * a.n + n0) * k;
     const Buffer wb = buffer_at(wt);
@@ -189,15 +206,13 @@ __global__ void __launch_bounds__(kConvWaves * 64, kWide ? 1 : 2) k_conv_tile(Pr
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       if (!group_has(have, j)) continue;
-      const int src = __shfl(entry, j * 16 + load_row, kWave);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         const int c = c0 + s * 64 + load_chunk;
         if constexpr (kDirect) {
-          load_to_lds(xb, ((src >= 0) & (c < k)) ? (unsigned)src * (unsigned)a.x_stride + c : kOutside, 0,
-                      my_x + (j * kSteps + s) * 1024);
-        } else if (src >= 0) {
-          const int8_t* row = a.x + src * a.x_stride;
+          load_to_lds(xb, (src[j] + c) | (c < k ? 0 : kOutside), 0, my_x + (j * kSteps + s) * 1024);
+        } else if ((int)src[j] >= 0) {
+          const int8_t* row = a.x + (int)src[j] * a.x_stride;
           x_held[j * kSteps + s] = k >= 16 ? load_16_end(row, c, k) : load_16_tail(row, c, k);
         }
       }
@@ -234,43 +249,63 @@ __global__ void __launch_bounds__(kConvWaves * 64, kWide ? 1 : 2) k_conv_tile(Pr
 #pragma unroll
     for (int i = 0; i < kWeightLoads; ++i) w_held[i] = v4i{0, 0, 0, 0};
   }
-  take_entry(0);
-  ask(0, 0, 0);
+  // the rows a lane loads, one of each group, as the lanes that own them have them: kDirect:
+  // byte offsets, otherwise their numbers; from 2^31 on: none
+  auto rows_of = [&](int entry, unsigned (&src)[kRows]) {
+    const unsigned at = entry < 0 ? kOutside : kDirect ? (unsigned)entry * (unsigned)a.x_stride : (unsigned)entry;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) src[j] = __shfl(at, j * 16 + load_row, kWave);
+  };
+  int entry = entry_at(0);
+  unsigned src[kRows];
+  unsigned long long have = __ballot(entry >= 0);
+  float scale = entry >= 0 ? a.x_scale[entry] : 0.0f;  // of this lane's row
+  rows_of(entry, src);
+  ask(0, 0, 0, have, src);
   put(0);
   int tap = 0, c0 = 0;
   for (int stage = 0; tap < taps; ++stage) {
+    const bool last = !kWide || c0 + 64 * kSteps >= k;  // of the tap
+    const int next_tap = last ? tap + 1 : tap, next_c0 = last ? 0 : c0 + 64 * kSteps;
+    const bool more = next_tap < taps;
+    const unsigned long long now = have;
+    if (last && more) {
+      entry = entry_at(next_tap);
+      have = __ballot(entry >= 0);
+      rows_of(entry, src);
+    }
     wait_loads<0>();
     meet();
     // this stage's operands and scales
-    const unsigned long long now = have;
-    v4i x[kRows][kSteps];
+    v4i x[kRows][kSteps], w[kPart][kSteps];
     float xs[kRows];
+    const int8_t* w_tile = s_w + (stage & 1) * BN * 64 * kSteps;
+    auto weights = [&](int part) {
+#pragma unroll
+      for (int t = 0; t < kPart; ++t) {
+        const int r = weight_row<kCols>(part * kPart + t, lr);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+          w[t][s] = *reinterpret_cast<const v4i*>(w_tile + (s * BN + r) * 64 + ((lc ^ weight_key<kCols>(r)) * 16));
+      }
+    };
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      if (!kWide || c0 + 64 * kSteps >= k) xs[j] = __shfl(scale, j * 16 + lr, kWave);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s)
         x[j][s] = *reinterpret_cast<const v4i*>(my_x + (j * kSteps + s) * 1024 + x_at);
+      xs[j] = last ? __shfl(scale, j * 16 + lr, kWave) : 0.0f;
     }
+    weights(0);
     wait_lds();  // the operands' LDS may be written again
-    const bool last = !kWide || c0 + 64 * kSteps >= k;  // of the tap
-    const int next_tap = last ? tap + 1 : tap, next_c0 = last ? 0 : c0 + 64 * kSteps;
-    if (next_tap < taps) {
-      if (last) take_entry(next_tap);
-      ask(next_tap, next_c0, (stage + 1) & 1);
+    if (more) {
+      if (last) scale = entry >= 0 ? a.x_scale[entry] : 0.0f;
+      ask(next_tap, next_c0, (stage + 1) & 1, have, src);
     }
-    const int8_t* w_tile = s_w + (stage & 1) * BN * 64 * kSteps;
     if (now) {
 #pragma unroll
       for (int part = 0; part < kCols / kPart; ++part) {
-        v4i w[kPart][kSteps];
-#pragma unroll
-        for (int t = 0; t < kPart; ++t) {
-          const int r = weight_row<kCols>(part * kPart + t, lr);
-#pragma unroll
-          for (int s = 0; s < kSteps; ++s)
-            w[t][s] = *reinterpret_cast<const v4i*>(w_tile + (s * BN + r) * 64 + ((lc ^ weight_key<kCols>(r)) * 16));
-        }
+        if (part > 0) weights(part);
 #pragma unroll
         for (int j = 0; j < kRows; ++j) {
           if (!group_has(now, j)) continue;
@@ -300,27 +335,162 @@ __global__ void __launch_bounds__(kConvWaves * 64, kWide ? 1 : 2) k_conv_tile(Pr
             for (int t = 0; t < kPart; ++t)
 #pragma unroll
               for (int i = 0; i < 4; ++i) acc[j][part * kPart + t][i] += xs[j] * (float)d[t][i];
+            __builtin_amdgcn_sched_group_barrier(0x008, kSteps * kPart, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, 8 * kPart, 0);
           }
         }
       }
     }
-    if (next_tap < taps) put((stage + 1) & 1);
+    if (more) put((stage + 1) & 1);
     tap = next_tap;
     c0 = next_c0;
   }
 
+  constexpr int kPair = kCols < 2 ? 1 : 2;  // instructions of one run of channels
 #pragma unroll
-  for (int part = 0; part < kCols / kPart; ++part) {
-    const Channels<kPart * 4> out(a, n0 + part * 64 + lc * 4 * kPart);
+  for (int t = 0; t < kCols; t += kPair) {
+    const Channels<kPair * 4> out(a, n0 + t * 16 + lc * 4 * kPair);
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
       const i64 row = row0 + s_order[(j * kConvWaves + wave) * 16 + lr];
       if (row >= a.rows) continue;
-      float v[kPart * 4];
+      float v[kPair * 4];
 #pragma unroll
-      for (int i = 0; i < kPart * 4; ++i) v[i] = acc[j][part * kPart + i / 4][i % 4];
+      for (int i = 0; i < kPair * 4; ++i) v[i] = acc[j][t + i / 4][i % 4];
       out.store(a, row, v);
     }
+  }
+}
+
+// Rows that do not fill the card in tiles of 256: 64 of them a workgroup, 16 a wave, and as
+// many taps a stage as registers take, so that their loads are under way together. The loads
+// of a stage (through registers, from any address) are asked for while the stage before is
+// computed; its weights are shared by the waves, in one buffer of LDS. At most 64 output
+// channels: with 128 the registers hold fewer workgroups a CU (14k rows, 100 -> 96: 44 us for 29).
+template <int kCols, int kSteps, bool kWide>
+__global__ void __launch_bounds__(kConvWaves * 64, kWide ? 2 : 3) k_conv_mid(ProductArgs a, int tiles_n) {
+  constexpr int kTaps = kCols * kSteps > 4 ? 3 : 4;  // of a stage
+  constexpr int BN = kCols * 16;
+  constexpr int kWeightParts = kTaps * kSteps * kCols;  // loads of 16 rows x 64 bytes
+  constexpr int kWeightLoads = (kWeightParts + kConvWaves - 1) / kConvWaves, kRowLoads = kTaps * kSteps;  // a wave
+  constexpr int kPair = kCols < 2 ? 1 : 2;
+  __shared__ __align__(16) int8_t s_all[(kWeightParts + kConvWaves * kRowLoads) * 1024];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lc = lane >> 4, load_row = lane >> 2;
+  const i64 tile = xcd_block(blockIdx.x, gridDim.x);
+  const i64 row = tile / tiles_n * (kConvWaves * 16) + wave * 16 + lr;
+  const int n0 = (int)(tile % tiles_n) * BN;
+  const int taps = a.taps, k = a.k;
+  int8_t* const my_x = s_all + (kWeightParts + wave * kRowLoads) * 1024;
+
+  // lane (u, r) of four by 16 holds the map entry and the scale of row r at tap u of the stage
+  const int32_t* my_map = a.map + min(row, a.rows - 1) * taps;
+  auto entry_at = [&](int tap0) {
+    const int e = my_map[min(tap0 + lc, taps - 1)];
+    return row < a.rows && lc < kTaps && tap0 + lc < taps && (uint32_t)e < (uint32_t)a.n_src ? e : -1;
+  };
+  v4i x_held[kRowLoads], w_held[kWeightLoads];
+#pragma unroll
+  for (int i = 0; i < kRowLoads; ++i) x_held[i] = v4i{0, 0, 0, 0};
+  auto ask = [&](int entry, int tap0, int c0) {
+#pragma unroll
+    for (int i = 0; i < kWeightLoads; ++i) {
+      const int part = i * kConvWaves + wave;
+      if (part < kWeightParts) {
+        const int r = part % kCols * 16 + load_row;
+        const int c = c0 + part / kCols % kSteps * 64 + ((lane & 3) ^ weight_key<kCols>(r)) * 16;
+        const int tap = min(tap0 + part / (kCols * kSteps), taps - 1);
+        const int8_t* from = a.w + ((i64)tap * a.n + min(n0 + r, a.n - 1)) * k;
+        w_held[i] = k >= 16 ? weight_16_end(from, c, k) : load_16_tail(from, c, k);
+      }
+    }
+    if (!__any(entry >= 0)) return;
+#pragma unroll
+    for (int u = 0; u < kTaps; ++u) {
+      // any row where there is none: its scale is zero
+      const int8_t* from = a.x + max(__shfl(entry, u * 16 + load_row, kWave), 0) * a.x_stride;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int c = c0 + s * 64 + ((lane & 3) ^ x_key(load_row)) * 16;
+        x_held[u * kSteps + s] = k >= 16 ? load_16_end(from, c, k) : load_16_tail(from, c, k);
+      }
+    }
+  };
+
+  v4f acc[kCols];
+  v4i dot[kWide ? kTaps : 1][kCols];
+#pragma unroll
+  for (int t = 0; t < kCols; ++t) {
+    acc[t] = v4f{0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < (kWide ? kTaps : 1); ++u) dot[u][t] = v4i{0, 0, 0, 0};
+  }
+  const int x_at = lr * 64 + ((lc ^ x_key(lr)) * 16);
+  int entry = entry_at(0), entry_ahead = entry_at(kTaps);
+  float scale = entry >= 0 ? a.x_scale[entry] : 0.0f;
+  ask(entry, 0, 0);
+  for (int tap0 = 0, c0 = 0; tap0 < taps;) {
+    const bool last = !kWide || c0 + 64 * kSteps >= k;  // of these taps
+    const int next_tap = last ? tap0 + kTaps : tap0, next_c0 = last ? 0 : c0 + 64 * kSteps;
+    const unsigned long long now = __ballot(entry >= 0);
+    meet();  // the stage before has been read
+#pragma unroll
+    for (int i = 0; i < kWeightLoads; ++i) {
+      const int part = i * kConvWaves + wave;
+      if (part < kWeightParts) *reinterpret_cast<v4i*>(s_all + part * 1024 + lane * 16) = w_held[i];
+    }
+#pragma unroll
+    for (int i = 0; i < kRowLoads; ++i) *reinterpret_cast<v4i*>(my_x + i * 1024 + lane * 16) = x_held[i];
+    float xs[kTaps];
+    if (last) {
+#pragma unroll
+      for (int u = 0; u < kTaps; ++u) xs[u] = __shfl(scale, u * 16 + lr, kWave);
+      entry = entry_ahead;
+      if (next_tap < taps) {
+        entry_ahead = entry_at(next_tap + kTaps);
+        scale = entry >= 0 ? a.x_scale[entry] : 0.0f;
+      }
+    }
+    meet();
+    if (next_tap < taps) ask(entry, next_tap, next_c0);
+#pragma unroll
+    for (int u = 0; u < kTaps; ++u) {
+      if (!(now >> (16 * u) & 0xffff)) continue;
+      v4i x[kSteps];
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) x[s] = *reinterpret_cast<const v4i*>(my_x + (u * kSteps + s) * 1024 + x_at);
+#pragma unroll
+      for (int t = 0; t < kCols; ++t) {
+        const int r = weight_row<kCols>(t, lr);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          const v4i w = *reinterpret_cast<const v4i*>(s_all + ((u * kSteps + s) * BN + r) * 64 +
+                                                      ((lc ^ weight_key<kCols>(r)) * 16));
+          v4i& d = dot[kWide ? u : 0][t];
+          d = product_16(w, x[s], !kWide && s == 0 ? v4i{0, 0, 0, 0} : d);
+        }
+      }
+      if (last) {
+#pragma unroll
+        for (int t = 0; t < kCols; ++t) {
+          v4i& d = dot[kWide ? u : 0][t];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][i] += xs[u] * (float)d[i];
+          if (kWide) d = v4i{0, 0, 0, 0};
+        }
+      }
+    }
+    tap0 = next_tap;
+    c0 = next_c0;
+  }
+  if (row >= a.rows) return;
+#pragma unroll
+  for (int t = 0; t < kCols; t += kPair) {
+    const Channels<kPair * 4> out(a, n0 + t * 16 + lc * 4 * kPair);
+    float v[kPair * 4];
+#pragma unroll
+    for (int i = 0; i < kPair * 4; ++i) v[i] = acc[t + i / 4][i % 4];
+    out.store(a, row, v);
   }
 }
 
@@ -404,47 +574,74 @@ void launch_conv(const ProductArgs& a, hipStream_t s) {
          ceil_div(a.rows, kConvWaves * kRows * 16) * tn, kConvWaves * 64, s, a, tn);
 }
 
+// The registers of a wave hold 64 rows x 128 channels of sums, except where the rows come
+// through registers as well, or integer sums are kept beside the float ones.
 template <int kCols>
-void launch_conv_few(const ProductArgs& a, hipStream_t s) {
+void conv_tile(const ProductArgs& a, bool direct, hipStream_t s) {
+  constexpr int kFew = std::min(kCols, 4);  // channels
+  if (a.k > 128) return direct ? launch_conv<4, kFew, 2, true, true>(a, s) : launch_conv<4, kFew, 2, false, true>(a, s);
+  if (a.k <= 64)
+    return direct ? launch_conv<4, kCols, 1, true, false>(a, s) : launch_conv<4, kCols, 1, false, false>(a, s);
+  if (direct) return launch_conv<4, kCols, 2, true, false>(a, s);
+  launch_conv<kCols == 8 ? 2 : 4, kCols, 2, false, false>(a, s);
+}
+
+template <int kCols, int kSteps, bool kWide>
+void launch_conv_mid(const ProductArgs& a, hipStream_t s) {
+  const int tn = (int)ceil_div(a.n, kCols * 16);
+  launch("k_conv_mid", k_conv_mid<kCols, kSteps, kWide>, ceil_div(a.rows, kConvWaves * 16) * tn, kConvWaves * 64, s, a,
+         tn);
+}
+template <int kCols>
+void conv_mid(const ProductArgs& a, hipStream_t s) {
+  if (a.k > 128) return launch_conv_mid<kCols, 2, true>(a, s);
+  if (a.k > 64) return launch_conv_mid<kCols, 2, false>(a, s);
+  launch_conv_mid<kCols, 1, false>(a, s);
+}
+
+template <int kCols>
+void conv_few(const ProductArgs& a, hipStream_t s) {
   const int tn = (int)ceil_div(a.n, kCols * 16);
   launch("k_conv_few", k_conv_few<kCols>, ceil_div(a.rows, 16) * tn, kFewWaves * 64, s, a, tn);
 }
 
-// The registers of a wave hold 64 rows x 128 channels of sums, except where the rows come
-// through registers as well, or integer sums are kept beside the float ones.
-template <int kRows, int kCols>
-void conv_tile(const ProductArgs& a, bool direct, hipStream_t s) {
-  if (a.k <= 64)
-    return direct ? launch_conv<kRows, kCols, 1, true, false>(a, s) : launch_conv<kRows, kCols, 1, false, false>(a, s);
-  if (a.k > 128) {
-    constexpr int kC = std::min(kCols, 4);
-    return direct ? launch_conv<kRows, kC, 2, true, true>(a, s) : launch_conv<kRows, kC, 2, false, true>(a, s);
-  }
-  if (direct) return launch_conv<kRows, kCols, 2, true, false>(a, s);
-  launch_conv<kCols == 8 ? std::min(kRows, 2) : kRows, kCols, 2, false, false>(a, s);
-}
-
-template <int kRows>
-void conv_rows(const ProductArgs& a, bool direct, hipStream_t s) {
-  if (a.n <= 16) return conv_tile<kRows, 1>(a, direct, s);
-  if (a.n <= 32) return conv_tile<kRows, 2>(a, direct, s);
-  if (a.n <= 64) return conv_tile<kRows, 4>(a, direct, s);
-  conv_tile<kRows, 8>(a, direct, s);
+// Calls f<kCols> for the channels of a tile.
+template <typename F>
+void with_cols(int n, F&& f) {
+  using std::integral_constant;
+  if (n <= 16) return f(integral_constant<int, 1>());
+  if (n <= 32) return f(integral_constant<int, 2>());
+  if (n <= 64) return f(integral_constant<int, 4>());
+  f(integral_constant<int, 8>());
 }
 
 }  // namespace
 
+// The variant. Timed over 27-tap maps of shells, bf16 out, in us a call:
+//   rows    channels     tile  middle  few
+//   116k    128 -> 128     69     164
+//   116k    64 -> 64       39      47
+//   65k     96 -> 96       55      85
+//   65k     64 -> 64       33      27
+//   37k     60 -> 60       45      24
+//   22k     100 -> 96      63      34  100
+//   5.5k    60 -> 96               19   23
+//   2.7k    60 -> 60               19   12
+// A tile of 256 rows reads its weights for four times the rows and skips more, and needs
+// about one workgroup a CU to be worth it; where it has 64 channels or fewer to share a row
+// among, more. Taps split over waves win while the rows leave CUs idle.
 void conv_i8(const ProductArgs& a, hipStream_t s) {
   const i64 cus = device_cu_count();
   auto tiles = [&](int rows, int cols) { return ceil_div(a.rows, rows) * ceil_div(a.n, cols); };
   // the offsets of a gather straight into LDS are 31 bits
   const bool direct = (((uintptr_t)a.x | (uintptr_t)a.x_stride | (uintptr_t)a.w | (uintptr_t)a.k) & 15) == 0 &&
                       a.n_src * a.x_stride + a.k < (1ll << 31);
-  if (tiles(256, 128) >= cus) return conv_rows<4>(a, direct, s);
-  if (tiles(64, 128) >= cus / 2) return conv_rows<1>(a, direct, s);
-  if (tiles(16, 64) >= cus) return launch_conv_few<4>(a, s);
-  if (tiles(16, 32) >= cus) return launch_conv_few<2>(a, s);
-  launch_conv_few<1>(a, s);
+  if (2 * tiles(256, 128) >= (a.n > 64 ? cus : 3 * cus))
+    return with_cols(a.n, [&](auto c) { conv_tile<decltype(c)::value>(a, direct, s); });
+  if (tiles(64, 64) >= cus / 2) return with_cols(a.n, [&](auto c) { conv_mid<std::min(decltype(c)::value, 4)>(a, s); });
+  if (tiles(16, 64) >= cus) return conv_few<4>(a, s);
+  if (tiles(16, 32) >= cus) return conv_few<2>(a, s);
+  conv_few<1>(a, s);
 }
 
 }  // namespace tc

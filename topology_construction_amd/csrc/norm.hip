@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kSumChannels* kSumSlices)
 
 // Workgroups whose parts of the weight gradient are joined at the end: enough to
 // have memory busy, while the parts stay small next to the rows.
-constexpr int kGradParts = 1024, kGradPartsWide = 512;
+constexpr int kGradParts = 1024, kGradPartsWide = 1024;
 int grad_parts(i64 rows, int channels) {
   return (int)std::max<i64>(1, std::min<i64>(rows, channels <= 512 ? kGradParts : kGradPartsWide));
 }

@@ -22,9 +22,13 @@ __device__ __forceinline__ void tile_place(i64 tile, i64 tiles_m, int tiles_n, i
   tn = at / size;
 }
 
-// Row r of the weights' tile t is channel (r / 4) * 16 + t * 4 + r % 4 of a wave's 64, so
-// that a lane's results of four tiles are 16 consecutive channels.
-__device__ __forceinline__ int w_key(int row) { return ((row >> 1) & 1) | ((row >> 3) & 2); }
+// Row r of the weights' matrix instruction t of a wave's 64 channels, such that a lane's
+// results of two instructions are 8 consecutive channels and the four lanes of an output
+// row store 64 bytes side by side; and the LDS slot key of such a row.
+__device__ __forceinline__ constexpr int w_row(int t, int r) {
+  return (t >> 1) * 32 + (r >> 2) * 8 + (t & 1) * 4 + (r & 3);
+}
+__device__ __forceinline__ int w_key(int row) { return ((row >> 1) & 1) | ((row >> 2) & 2); }
 
 // BM x BN outputs per workgroup, (BM / WM) * (BN / 64) waves of WM x 64 each, in
 // steps of 64 input channels. kDirect: rows and chunks on 16-byte boundaries go
@@ -37,7 +41,12 @@ __global__ void __launch_bounds__((BM / WM) * (BN / 64) * 64)
   constexpr int kWaves = (BM / WM) * (BN / 64);
   constexpr int kLoads = (BM + BN) / 16 / kWaves;  // per wave and step
   constexpr int kBuf = (BM + BN) * 64;
-  __shared__ __align__(16) int8_t s_tiles[kBufs * kBuf];
+  // One array: with several the compiler has every read of a tile wait for all loads
+  // under way into any of them. Behind the tiles are the scales, read before the loop for its end.
+  __shared__ __align__(16) int8_t s_tiles[kBufs * kBuf + (2 * BN + BM) * 4];
+  float* const s_scale = reinterpret_cast<float*>(s_tiles + kBufs * kBuf);
+  float* const s_bias = s_scale + BN;
+  float* const s_rows = s_bias + BN;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   i64 tm;
   int tn;
@@ -92,13 +101,13 @@ __global__ void __launch_bounds__((BM / WM) * (BN / 64) * 64)
 #pragma unroll
     for (int t = 0; t < 4; ++t) dot[j][t] = v4i{0, 0, 0, 0};
   // the keys depend on neither t nor j
-  const int wr = wn + (lr >> 2) * 16 + (lr & 3), xr = wm + lr;
+  const int wr = wn + w_row(0, lr), xr = wm + lr;
   const int w_at = BM * 64 + wr * 64 + ((lc ^ w_key(wr)) * 16), x_at = xr * 64 + ((lc ^ x_key(xr)) * 16);
   auto multiply = [&](int step) {
     const int8_t* tile = s_tiles + (step % kBufs) * kBuf;
     v4i w[4], x[kRows];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) w[t] = *reinterpret_cast<const v4i*>(tile + w_at + t * 256);
+    for (int t = 0; t < 4; ++t) w[t] = *reinterpret_cast<const v4i*>(tile + w_at + w_row(t, 0) * 64);
 #pragma unroll
     for (int j = 0; j < kRows; ++j) x[j] = *reinterpret_cast<const v4i*>(tile + x_at + j * 1024);
 #pragma unroll
@@ -114,10 +123,28 @@ __global__ void __launch_bounds__((BM / WM) * (BN / 64) * 64)
     }
     __builtin_amdgcn_sched_group_barrier(0x008, kRows > 2 ? 8 : 4 * kRows, 0);
   };
+  const int tid = threadIdx.x;
+  float scale = 0.0f, bias = 0.0f, row_scale = 0.0f;
+  if (tid < BN) {
+    const int c = min(n0 + tid, a.n - 1);
+    scale = a.w_scale[c];
+    if (a.bias) bias = a.bias[c];
+  }
+  if (tid < BM) row_scale = a.x_scale[min(row0 + tid, a.rows - 1)];
+  auto put_scales = [&]() {
+    if (tid < BN) {
+      s_scale[tid] = scale;
+      s_bias[tid] = bias;
+    }
+    if (tid < BM) s_rows[tid] = row_scale;
+  };
+  static_assert(kWaves * 64 >= BN && kWaves * 64 >= BM, "one thread per channel and per row");
+
   if constexpr (kDirect) {
 #pragma unroll
     for (int s = 0; s < kBufs - 1; ++s)
       if (s < steps) issue(s, true);
+    put_scales();
     int s = 0;
     for (; s + kBufs < steps; ++s) {
       wait_loads<(kBufs - 2) * kLoads>();  // the loads of the steps after s may be under way
@@ -138,6 +165,7 @@ __global__ void __launch_bounds__((BM / WM) * (BN / 64) * 64)
     }
   } else {
     load(0);
+    put_scales();
     put(0);
     if (steps > 1) load(1);
     for (int s = 0; s < steps; ++s) {
@@ -148,24 +176,26 @@ __global__ void __launch_bounds__((BM / WM) * (BN / 64) * 64)
     }
   }
 
-  const int n = n0 + wn + lc * 16;
-  float ws[16], b[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int c = min(n + i, a.n - 1);
-    ws[i] = a.w_scale[c];
-    b[i] = a.bias ? a.bias[c] : 0.0f;
-  }
   const bool wide = ((((uintptr_t)a.out) | (a.out_stride * sizeof(T))) & 15) == 0;
 #pragma unroll
-  for (int j = 0; j < WM / 16; ++j) {
-    const i64 row = row0 + wm + j * 16 + lr;
-    if (row >= a.rows) continue;
-    const float xs = a.x_scale[row];
-    float v[16];
+  for (int h = 0; h < 2; ++h) {
+    const int c = wn + h * 32 + lc * 8;
+    float ws[8], b[8];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = xs * (float)dot[j][i >> 2][i & 3] * ws[i] + b[i];
-    store_run<T, 16>(a, row, n, v, wide);
+    for (int i = 0; i < 8; ++i) {
+      ws[i] = s_scale[c + i];
+      b[i] = s_bias[c + i];
+    }
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const i64 row = row0 + wm + j * 16 + lr;
+      if (row >= a.rows) continue;
+      const float xs = s_rows[wm + j * 16 + lr];
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = xs * (float)dot[j][h * 2 + (i >> 2)][i & 3] * ws[i] + b[i];
+      store_run<T, 8>(a, row, n0 + c, v, wide);
+    }
   }
 }
 

@@ -29,6 +29,10 @@ __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), kCtrl, 0xf, 0xf, true));
 }
 template <int kCtrl>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, kCtrl, 0xf, 0xf, true);
+}
+template <int kCtrl>
 __device__ __forceinline__ double dpp(double v) {
   return __hiloint2double(__builtin_amdgcn_mov_dpp(__double2hiint(v), kCtrl, 0xf, 0xf, true),
                           __builtin_amdgcn_mov_dpp(__double2loint(v), kCtrl, 0xf, 0xf, true));
