@@ -515,44 +515,33 @@ def tc_build_kernel_map_noalloc(src: GridBatch, dst: GridBatch, kernel_size: int
 
 
 # -- operators on feature rows ------------------------------------------------
-# A call of one row takes the GPU a few microseconds, and the host about as long: what a
-# call looks up is kept here, and each tensor is asked for each of its properties once.
+# A call of one row takes the GPU about five microseconds; checking tensors and taking outputs
+# from here took the host more than that, so csrc/bind.cpp does both (_features.so).
 class _Ops:
     def __init__(self):
         import torch
-        self.lib = load_library()
-        self.ids = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}  # tc_dtype
-        self.f32, self.i8, self.i32, self.u8 = torch.float32, torch.int8, torch.int32, torch.uint8
-        self.bf16 = torch.bfloat16
-        self.current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        load_library()
+        try:
+            from . import _features as f
+        except ImportError as e:
+            raise ImportError(f"_features.so is missing or does not load ({e}): build it with "
+                              "`python -m topology_construction_amd.build`") from e
+        f.set_error(TopoError)
+        self.rms_norm, self.rms_norm_i8, self.rms_norm_backward = f.rms_norm, f.rms_norm_i8, f.rms_norm_backward
+        self.matmul_i8, self.sparse_conv_i8 = f.matmul_i8, f.sparse_conv_i8
         self.on_stream = torch.cuda.stream
-        self.raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if self.raw_stream is None:
-            self.raw_stream = lambda device: torch.cuda.current_stream(device).cuda_stream
+        # without a GPU no tensor passes the checks, whatever the device
+        self.device = getattr(torch._C, "_cuda_getDevice") if torch.cuda.is_available() else lambda: -1
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.stream = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
-    def dtype_id(self, dtype) -> int:
-        i = self.ids.get(dtype)
-        if i is None:
-            raise TypeError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
-        return i
-
-    def device_of(self, t) -> int:
-        d = t.get_device()
-        if d < 0:
-            raise TypeError("the tensors must be cuda tensors")
-        if d != self.current_device():
-            raise ValueError("the tensors are not on the current device")
-        return d
-
-    def stream(self, stream, device: int) -> int:
-        return self.raw_stream(device) if stream is None else stream.cuda_stream
-
-    def empty(self, like, shape, dtype, stream):
-        """A tensor on the device of `like`, taken on the stream the library writes it on."""
+    def call(self, f, stream, *args):
+        """f on the current stream, or on `stream`: outputs are taken on the stream they are written on."""
+        device = self.device()
         if stream is None:
-            return like.new_empty(shape, dtype=dtype)
+            return f(*args, device, self.stream(device) if device >= 0 else 0)
         with self.on_stream(stream):
-            return like.new_empty(shape, dtype=dtype)
+            return f(*args, device, stream.cuda_stream)
 
 
 _ops_state = None
@@ -565,79 +554,19 @@ def _ops() -> _Ops:
     return _ops_state
 
 
-def _check_kind(t, name: str, dtype, device: int):
-    if t.dtype is not dtype or t.get_device() != device:
-        if not t.is_cuda or t.dtype is not dtype:
-            raise TypeError(f"{name} must be a cuda {dtype} tensor")
-        raise ValueError("the tensors are on different devices")
-
-
-def _matrix(t, name: str, dtype, device: int, rows=None, cols=None):
-    """A device matrix with unit channel stride (any row stride) as (pointer, row stride)."""
-    _check_kind(t, name, dtype, device)
-    shape = t.shape
-    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (cols is not None and shape[1] != cols):
-        raise ValueError(f"{name} has shape {tuple(shape)}, expected [{'rows' if rows is None else rows}, "
-                         f"{'channels' if cols is None else cols}]")
-    stride, unit = t.stride()
-    if unit != 1 and shape[1] > 1:
-        raise ValueError(f"{name} must have unit channel stride")
-    return t.data_ptr(), stride
-
-
-def _vector(t, name: str, dtype, device: int, n: int) -> int:
-    _check_kind(t, name, dtype, device)
-    shape = t.shape
-    if len(shape) != 1 or shape[0] != n or (n > 1 and t.stride()[0] != 1):
-        raise ValueError(f"{name} must be a contiguous vector of {n}")
-    return t.data_ptr()
-
-
-def _norm_inputs(ops, x, weight, residual):
-    dtype = x.dtype
-    wdt = dt = ops.dtype_id(dtype)
-    dev = ops.device_of(x)
-    px, sx = _matrix(x, "x", dtype, dev)
-    rows, channels = x.shape
-    pr, sr = _matrix(residual, "residual", dtype, dev, rows, channels) if residual is not None else (None, 0)
-    pw = None
-    if weight is not None:
-        wdt = ops.dtype_id(weight.dtype)
-        pw = _vector(weight, "weight", weight.dtype, dev, channels)
-    return px, sx, pr, sr, pw, wdt, rows, channels, dt, dev
-
-
 def tc_rms_norm(x, weight=None, residual=None, eps: float = 1e-6, stream=None):
     """Root-mean-square norm of rows: h = x + residual, s = 1 / sqrt(mean(h^2) + eps),
     out = h * s * weight. Returns (out, h, rstd): h is x itself without a residual,
     rstd float32 [rows] is s, kept for tc_rms_norm_backward."""
     ops = _ops()
-    px, sx, pr, sr, pw, wdt, rows, channels, dt, dev = _norm_inputs(ops, x, weight, residual)
-    out = ops.empty(x, (rows, channels), x.dtype, stream)
-    rstd = ops.empty(x, (rows,), ops.f32, stream)
-    h, ph = x, None
-    if residual is not None:
-        h = ops.empty(x, (rows, channels), x.dtype, stream)
-        ph = h.data_ptr()
-    _check(ops.lib.tc_rms_norm(px, sx, pr, sr, pw, wdt, rows, channels, dt, eps, ph, out.data_ptr(), rstd.data_ptr(),
-                               ops.stream(stream, dev)))
-    return out, h, rstd
+    return ops.call(ops.rms_norm, stream, x, weight, residual, eps)
 
 
 def tc_rms_norm_i8(x, weight=None, residual=None, eps: float = 1e-6, stream=None):
     """The norm with an 8-bit output: (q int8 [rows, channels], scale float32 [rows], h),
     q * scale standing for h * s * weight."""
     ops = _ops()
-    px, sx, pr, sr, pw, wdt, rows, channels, dt, dev = _norm_inputs(ops, x, weight, residual)
-    q = ops.empty(x, (rows, channels), ops.i8, stream)
-    scale = ops.empty(x, (rows,), ops.f32, stream)
-    h, ph = x, None
-    if residual is not None:
-        h = ops.empty(x, (rows, channels), x.dtype, stream)
-        ph = h.data_ptr()
-    _check(ops.lib.tc_rms_norm_i8(px, sx, pr, sr, pw, wdt, rows, channels, dt, eps, ph, q.data_ptr(), scale.data_ptr(),
-                                  ops.stream(stream, dev)))
-    return q, scale, h
+    return ops.call(ops.rms_norm_i8, stream, x, weight, residual, eps)
 
 
 def tc_rms_norm_backward(grad_out, h, weight, rstd, grad_h=None, stream=None):
@@ -645,50 +574,7 @@ def tc_rms_norm_backward(grad_out, h, weight, rstd, grad_h=None, stream=None):
     the gradient of x and of the residual alike, `grad_h` (if given) that of h by its
     other uses; grad_weight is float32 [channels], None without a weight."""
     ops = _ops()
-    dtype = h.dtype
-    wdt = dt = ops.dtype_id(dtype)
-    dev = ops.device_of(h)
-    ph, sh = _matrix(h, "h", dtype, dev)
-    rows, channels = h.shape
-    pg, sg = _matrix(grad_out, "grad_out", dtype, dev, rows, channels)
-    pd, sd = _matrix(grad_h, "grad_h", dtype, dev, rows, channels) if grad_h is not None else (None, 0)
-    ps = _vector(rstd, "rstd", ops.f32, dev, rows)
-    pw, grad_weight, pgw, work, pwork, nbytes = None, None, None, None, None, 0
-    if weight is not None:
-        wdt = ops.dtype_id(weight.dtype)
-        pw = _vector(weight, "weight", weight.dtype, dev, channels)
-        grad_weight = ops.empty(h, (channels,), ops.f32, stream)
-        pgw = grad_weight.data_ptr()
-        nbytes = ops.lib.tc_rms_norm_backward_workspace(rows, channels)
-        work = ops.empty(h, (max(nbytes, 1),), ops.u8, stream)
-        pwork = work.data_ptr()
-    grad_x = ops.empty(h, (rows, channels), dtype, stream)
-    _check(ops.lib.tc_rms_norm_backward(pg, sg, pd, sd, ph, sh, pw, wdt, ps, rows, channels, dt, grad_x.data_ptr(), pgw,
-                                        pwork, nbytes, ops.stream(stream, dev)))
-    return grad_x, grad_weight
-
-
-def _product_inputs(ops, x, x_scale, w_scale, c_out, bias):
-    dev = ops.device_of(x)
-    px, sx = _matrix(x, "x", ops.i8, dev)
-    rows, c_in = x.shape
-    xs = _vector(x_scale, "x_scale", ops.f32, dev, rows)
-    ws = _vector(w_scale, "w_scale", ops.f32, dev, c_out)
-    pb = _vector(bias, "bias", ops.f32, dev, c_out) if bias is not None else None
-    return px, sx, xs, ws, pb, rows, c_in, dev
-
-
-def _product_out(ops, x, out, rows, channels, out_dtype, device, stream):
-    """(out, its dtype, pointer, row stride)."""
-    if out is None:
-        dt = ops.dtype_id(out_dtype or ops.bf16)
-        out = ops.empty(x, (rows, channels), out_dtype or ops.bf16, stream)
-        return out, dt, out.data_ptr(), channels
-    dt = ops.dtype_id(out.dtype)
-    ptr, stride = _matrix(out, "out", out.dtype, device, rows, channels)
-    if stride < channels and rows > 1:
-        raise ValueError("the rows of out overlap")
-    return out, dt, ptr, max(stride, channels)
+    return ops.call(ops.rms_norm_backward, stream, grad_out, h, weight, rstd, grad_h)
 
 
 def tc_matmul_i8(x, x_scale, w, w_scale, bias=None, out_dtype=None, out=None, stream=None):
@@ -696,12 +582,7 @@ def tc_matmul_i8(x, x_scale, w, w_scale, bias=None, out_dtype=None, out=None, st
     scales for each row and each output channel, float32 bias [c_out]: [rows, c_out]
     of `out_dtype` (bfloat16 unless given), or into `out` (any row stride)."""
     ops = _ops()
-    c_out = w.shape[0]
-    px, sx, xs, ws, pb, rows, c_in, dev = _product_inputs(ops, x, x_scale, w_scale, c_out, bias)
-    pw, sw = _matrix(w, "w", ops.i8, dev, c_out, c_in)
-    out, dt, po, so = _product_out(ops, x, out, rows, c_out, out_dtype, dev, stream)
-    _check(ops.lib.tc_matmul_i8(px, sx, xs, pw, sw, ws, pb, rows, c_out, c_in, dt, po, so, ops.stream(stream, dev)))
-    return out
+    return ops.call(ops.matmul_i8, stream, x, x_scale, w, w_scale, bias, out_dtype, out)
 
 
 def tc_sparse_conv_i8(x, x_scale, kmap, w, w_scale, bias=None, out_dtype=None, out=None, stream=None):
@@ -709,21 +590,7 @@ def tc_sparse_conv_i8(x, x_scale, kmap, w, w_scale, bias=None, out_dtype=None, o
     tc_build_kernel_map returns it) with int8 weights w [taps, c_out, c_in]; scales,
     bias and output as for tc_matmul_i8."""
     ops = _ops()
-    if w.dim() != 3:
-        raise ValueError("w must be a contiguous [taps, c_out, c_in] tensor")
-    wt, c_out, wk = w.shape
-    px, sx, xs, ws, pb, n_src, c_in, dev = _product_inputs(ops, x, x_scale, w_scale, c_out, bias)
-    _check_kind(kmap, "kmap", ops.i32, dev)
-    if kmap.dim() != 2 or not kmap.is_contiguous():
-        raise ValueError("kmap must be a contiguous [n_dst, taps] tensor")
-    n_dst, taps = kmap.shape
-    _check_kind(w, "w", ops.i8, dev)
-    if wt != taps or wk != c_in or not w.is_contiguous():
-        raise ValueError(f"w must be a contiguous [{taps}, c_out, {c_in}] tensor")
-    out, dt, po, so = _product_out(ops, x, out, n_dst, c_out, out_dtype, dev, stream)
-    _check(ops.lib.tc_sparse_conv_i8(px, sx, xs, n_src, kmap.data_ptr(), n_dst, taps, w.data_ptr(), ws, pb, c_out,
-                                     c_in, dt, po, so, ops.stream(stream, dev)))
-    return out
+    return ops.call(ops.sparse_conv_i8, stream, x, x_scale, kmap, w, w_scale, bias, out_dtype, out)
 
 
 def tc_scratch_release():

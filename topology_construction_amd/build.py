@@ -1,4 +1,5 @@
-"""Compile the HIP sources into libtopo.so (gfx950), in-tree.
+"""Compile the HIP sources into libtopo.so (gfx950) and the torch side of the operators on
+feature rows into _features.so (host code over libtopo.so's C ABI), in-tree.
 
 Usage: python -m topology_construction_amd.build [--jobs N]
 Every call recompiles (it is the build check); objects go to _build/.
@@ -10,11 +11,13 @@ import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libtopo.so")
+FEATURES = os.path.join(HERE, "_features.so")
 ARCH = os.environ.get("TOPO_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
@@ -49,7 +52,24 @@ def build(jobs: int | None = None) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _build_features()
     return LIB
+
+
+def _build_features() -> None:
+    import torch
+    from torch.utils import cpp_extension
+    tmp = FEATURES + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-Wno-unused-function",
+           "-DUSE_ROCM", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + os.path.join(os.path.dirname(HERE), "include"), "-I" + sysconfig.get_paths()["include"],
+           *("-I" + p for p in cpp_extension.include_paths()), os.path.join(CSRC, "bind.cpp"), "-o", tmp,
+           *("-L" + p for p in cpp_extension.library_paths()), "-lc10", "-ltorch_cpu", "-ltorch_python",
+           "-L" + HERE, "-l:libtopo.so", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for bind.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FEATURES)
 
 
 def clean() -> None:
