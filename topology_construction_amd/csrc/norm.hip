@@ -54,6 +54,38 @@ struct RowPlace {
   }
 };
 
+// A row's vectors, loaded where the place has any.
+template <typename T, int L, int N>
+__device__ __forceinline__ void load_row(Vec<T> (&v)[N], const RowPlace<T, L, N>& at, const void* base, i64 offset) {
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    if (at.c[j] >= 0) v[j].load(static_cast<const T*>(base) + offset + at.c[j]);
+}
+
+// The weights of a place's elements (T's type, or 32 bits; ones without any; 0 where there is no element).
+template <typename T, int L, int N>
+__device__ __forceinline__ void load_weights(float (&w)[N][Vec<T>::kN], const RowPlace<T, L, N>& at, const void* p,
+                                             int dtype) {
+  constexpr int V = Vec<T>::kN;
+  Vec<T> raw[N];
+  float wide[N][V];
+  if (p && dtype == TC_F32) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (at.c[j] >= 0) __builtin_memcpy(wide[j], static_cast<const float*>(p) + at.c[j], V * 4);
+  } else if (p) {
+    load_row<T, L, N>(raw, at, p, 0);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int e = 0; e < V; ++e) wide[j][e] = to_f32(raw[j].v[e]);
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[j][e] = at.c[j] < 0 ? 0.0f : p ? wide[j][e] : 1.0f;
+}
+
 // Sums over the L threads of a group, L a power of two up to a wave, or a workgroup of
 // four waves. Every thread gets the sum, in an order that only L decides.
 struct GroupScratch {
@@ -117,30 +149,26 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm(NormArgs a) {
   constexpr int V = Vec<T>::kN;
   __shared__ GroupScratch s_red;
   const RowPlace<T, L, N> at(a.channels);
+  const i64 step = (i64)gridDim.x * (kNormThreads / L);
+  i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L;
+  Vec<T> x[N], r[N];  // of the next row, asked for before the row at hand is reduced
+  auto ask = [&](i64 row) {
+    if (row >= a.rows) return;
+    load_row<T, L, N>(x, at, a.x, row * a.x_stride);
+    if (a.residual) load_row<T, L, N>(r, at, a.residual, row * a.residual_stride);
+  };
+  ask(row);
   float w[N][V];
-#pragma unroll
-  for (int j = 0; j < N; ++j)
-#pragma unroll
-    for (int e = 0; e < V; ++e) w[j][e] = at.c[j] >= 0 ? weight_at(a.weight, a.weight_dtype, at.c[j] + e) : 0.0f;
+  load_weights<T, L, N>(w, at, a.weight, a.weight_dtype);
   int turn = 0;
-  for (i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L; row < a.rows;
-       row += (i64)gridDim.x * (kNormThreads / L), turn ^= 1) {
-    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+  for (; row < a.rows; row += step, turn ^= 1) {
     Vec<T> h[N];
 #pragma unroll
     for (int j = 0; j < N; ++j)
-      if (at.c[j] >= 0) h[j].load(x + at.c[j]);
-    if (a.residual) {
-      const T* r = static_cast<const T*>(a.residual) + row * a.residual_stride;
-      Vec<T> v[N];
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (at.c[j] >= 0) v[j].load(r + at.c[j]);
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-#pragma unroll
-        for (int e = 0; e < V; ++e) h[j].v[e] = from_f32<T>(to_f32(h[j].v[e]) + to_f32(v[j].v[e]));
-    }
+      for (int e = 0; e < V; ++e)
+        h[j].v[e] = a.residual ? from_f32<T>(to_f32(x[j].v[e]) + to_f32(r[j].v[e])) : x[j].v[e];
+    ask(row + step);
     float ss = 0.0f;
     double top = 0.0;
 #pragma unroll
@@ -200,33 +228,35 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad(NormGradArgs a) 
   constexpr int V = Vec<T>::kN;
   __shared__ GroupScratch s_red;
   const RowPlace<T, L, N> at(a.channels);
+  const i64 step = (i64)gridDim.x * (kNormThreads / L);
+  i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L;
+  Vec<T> next_dy[N], next_h[N], next_dh[N];  // of the next row
+  float next_rstd = 0.0f;
+  auto ask = [&](i64 row) {
+    if (row >= a.rows) return;
+    load_row<T, L, N>(next_dy, at, a.grad_out, row * a.grad_out_stride);
+    load_row<T, L, N>(next_h, at, a.h, row * a.h_stride);
+    if (a.grad_sum) load_row<T, L, N>(next_dh, at, a.grad_sum, row * a.grad_sum_stride);
+    next_rstd = a.rstd[row];
+  };
+  ask(row);
   float w[N][V], dw[N][V];
+  load_weights<T, L, N>(w, at, a.weight, a.weight_dtype);
 #pragma unroll
   for (int j = 0; j < N; ++j)
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      w[j][e] = at.c[j] >= 0 ? weight_at(a.weight, a.weight_dtype, at.c[j] + e) : 0.0f;
-      dw[j][e] = 0.0f;
-    }
+    for (int e = 0; e < V; ++e) dw[j][e] = 0.0f;
   int turn = 0;
-  for (i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L; row < a.rows;
-       row += (i64)gridDim.x * (kNormThreads / L), turn ^= 1) {
-    const T* pdy = static_cast<const T*>(a.grad_out) + row * a.grad_out_stride;
-    const T* ph = static_cast<const T*>(a.h) + row * a.h_stride;
+  for (; row < a.rows; row += step, turn ^= 1) {
     Vec<T> dy[N], h[N], dh[N];
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      if (at.c[j] < 0) continue;
-      dy[j].load(pdy + at.c[j]);
-      h[j].load(ph + at.c[j]);
+      dy[j] = next_dy[j];
+      h[j] = next_h[j];
+      dh[j] = next_dh[j];
     }
-    if (a.grad_sum) {
-      const T* pdh = static_cast<const T*>(a.grad_sum) + row * a.grad_sum_stride;
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (at.c[j] >= 0) dh[j].load(pdh + at.c[j]);
-    }
-    const float rstd = a.rstd[row];
+    const float rstd = next_rstd;
+    ask(row + step);
     float dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
