@@ -32,9 +32,16 @@ __device__ __forceinline__ int w_key(int row) { return ((row >> 1) & 1) | ((row 
 
 // BM x BN outputs per workgroup, (BM / WM) * (BN / 64) waves of WM x 64 each, in
 // steps of 64 input channels. kDirect: rows and chunks on 16-byte boundaries go
-// straight into LDS, kBufs - 1 steps ahead of the products. Otherwise, from any
+// straight into LDS, kBufs - 1 steps ahead of the products, or (kPer = 2, four buffers)
+// two steps between barriers, with the loads of the next two under way. Otherwise, from any
 // address, through registers: loaded two steps ahead, written one step ahead.
-template <typename T, int BM, int BN, int WM, int kBufs, bool kDirect>
+//
+// 16384 x 4096 -> 4096: 233 us, 2360 TOP/s (a library's 8-bit product of this size: 1990): the
+// matrix units are busy 56% of the cycles at the 2.0 GHz the card holds under this load.
+// One barrier a step: 248 us; loads spread among the products instead of after the
+// barrier: 243; the second step's reads among the first's products: no change.
+// 124800 x 256 -> 768: 57 us, 224 MB at 3.9 TB/s: bound by the stores (33 us without them).
+template <typename T, int BM, int BN, int WM, int kBufs, int kPer, bool kDirect>
 __global__ void __launch_bounds__((BM / WM) * (BN / 64) * 64)
     k_product_tile(ProductArgs a, i64 tiles_m, int tiles_n) {
   static_assert(kDirect || kBufs == 2, "one buffer is read, one written");
@@ -140,7 +147,28 @@ __global__ void __launch_bounds__((BM / WM) * (BN / 64) * 64)
   };
   static_assert(kWaves * 64 >= BN && kWaves * 64 >= BM, "one thread per channel and per row");
 
-  if constexpr (kDirect) {
+  if constexpr (kDirect && kPer == 2) {
+    issue(0, true);
+    if (steps > 1) issue(1, true);
+    put_scales();
+    int s = 0;
+    for (; s + 4 < steps; s += 2) {
+      wait_loads<0>();
+      meet();
+      issue(s + 2, false);
+      issue(s + 3, false);
+      multiply(s);
+      multiply(s + 1);
+    }
+    for (; s < steps; s += 2) {
+      wait_loads<0>();
+      meet();
+      if (s + 2 < steps) issue(s + 2, true);
+      if (s + 3 < steps) issue(s + 3, true);
+      multiply(s);
+      if (s + 1 < steps) multiply(s + 1);
+    }
+  } else if constexpr (kDirect) {
 #pragma unroll
     for (int s = 0; s < kBufs - 1; ++s)
       if (s < steps) issue(s, true);
@@ -290,11 +318,11 @@ __global__ void __launch_bounds__(kFewWaves * 64) k_product_few(ProductArgs a) {
   }
 }
 
-template <typename T, int BM, int BN, int WM, int kBufs, bool kDirect>
+template <typename T, int BM, int BN, int WM, int kBufs, int kPer, bool kDirect>
 void launch_tile(const ProductArgs& a, hipStream_t s) {
   const i64 tm = ceil_div(a.rows, BM);
   const int tn = (int)ceil_div(a.n, BN);
-  launch("k_product_tile", k_product_tile<T, BM, BN, WM, kBufs, kDirect>, tm * tn, (BM / WM) * (BN / 64) * 64, s, a,
+  launch("k_product_tile", k_product_tile<T, BM, BN, WM, kBufs, kPer, kDirect>, tm * tn, (BM / WM) * (BN / 64) * 64, s, a,
          tm, tn);
 }
 
@@ -309,15 +337,15 @@ bool aligned_16(const void* p, i64 stride) { return (((uintptr_t)p | (uintptr_t)
 // The variant of a plain product. Timed at 16384 x 4096 -> 4096 (a), 124800 x 256 -> 768 (b),
 // 2048 x 1024 -> 1024 (c), 100 x 4096 -> 4096 (d), 64 x 1024 -> 1024 (e), bf16 out, in us:
 //   tile        256x256  256x128  64x64  few rows (best split)
-//   (a)             236      272    539     -
-//   (b)              66       60     88   347
-//   (c)              18       12    9.1    17
-//   (d)              44       29     19    14
-//   (e)              15       10    7.2   4.0
+//   (a)             233      284    542  1415
+//   (b)              61       57     82   383
+//   (c)              16       12    8.8    18
+//   (d)              43       28     19    15
+//   (e)              13       10    7.0   5.6
 // A tile's loads and products grow as its area, its traffic as its edge: the largest tile that
 // fills the card is best, but 256 x 256 runs one workgroup a CU, whose stores nothing hides
 // when the input channels are few. Through registers (unaligned) the order is the same
-// ((a) with 4095 input channels: 304, 380, 799).
+// ((a) with 4095 input channels: 296, 390, 842).
 template <typename T>
 void plain_product(const ProductArgs& a, hipStream_t s) {
   const i64 cus = device_cu_count();
@@ -325,11 +353,11 @@ void plain_product(const ProductArgs& a, hipStream_t s) {
   const bool direct = aligned_16(a.x, a.x_stride) && aligned_16(a.w, a.w_stride) && a.k % 16 == 0 &&
                       std::max(a.x_stride, a.w_stride) < (1 << 22);  // a tile's offsets stay below 2^31
   if (a.k >= 1024 && tiles(256, 256) >= cus + cus / 2)
-    return direct ? launch_tile<T, 256, 256, 128, 3, true>(a, s) : launch_tile<T, 256, 256, 128, 2, false>(a, s);
+    return direct ? launch_tile<T, 256, 256, 128, 4, 2, true>(a, s) : launch_tile<T, 256, 256, 128, 2, 1, false>(a, s);
   if (tiles(256, 128) >= cus)
-    return direct ? launch_tile<T, 256, 128, 64, 3, true>(a, s) : launch_tile<T, 256, 128, 64, 2, false>(a, s);
+    return direct ? launch_tile<T, 256, 128, 64, 3, 1, true>(a, s) : launch_tile<T, 256, 128, 64, 2, 1, false>(a, s);
   if (tiles(64, 64) > cus / 2)
-    return direct ? launch_tile<T, 64, 64, 32, 4, true>(a, s) : launch_tile<T, 64, 64, 32, 2, false>(a, s);
+    return direct ? launch_tile<T, 64, 64, 32, 4, 1, true>(a, s) : launch_tile<T, 64, 64, 32, 2, 1, false>(a, s);
   // few tiles: the most sharing that still gives every CU a workgroup
   if (tiles(64, 32) >= cus) return launch_few<T, 4, 2>(a, s);
   if (tiles(32, 32) >= cus) return launch_few<T, 2, 2>(a, s);
