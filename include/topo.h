@@ -344,8 +344,8 @@ tc_status tc_build_kernel_map_noalloc(const tc_grid_batch* src, const tc_grid_ba
  * Conventions: matrices are row-major with unit channel stride; an input's
  * `*_stride` is the distance between rows in elements (at least 0: a stride of
  * 0 repeats one row), outputs without a stride are contiguous. No alignment
- * beyond the element's own is required; rows that start on 16-byte boundaries
- * take the wide loads. Nothing is allocated and nothing blocks: the calls may be
+ * beyond the element's own is required; 8-bit rows and weights on 16-byte boundaries
+ * take shorter paths to the same results. Nothing is allocated and nothing blocks: the calls may be
  * captured into a HIP graph. An output may not overlap an input, except where
  * said. A pointer whose array is empty may be NULL. Channels are 1 to 2^20. */
 typedef enum tc_dtype { TC_F32 = 0, TC_F16 = 1, TC_BF16 = 2 } tc_dtype;
@@ -382,7 +382,7 @@ tc_status tc_rms_norm_i8(const void* d_x, int64_t x_stride, const void* d_residu
  * uses (the residual stream) and g = dy w:
  *   grad_x = s g - h s^3 mean(g h) + dh, rounded to dtype: the gradient of x, and of r alike;
  *   grad_weight = sum over rows of dy h s, a 32-bit float sum in an order that
- *   only n_rows and channels decide.
+ *   only n_rows, channels and dtype decide.
  *   d_grad_out   dtype[n_rows][channels], grad_out_stride.
  *   d_grad_sum   dh, dtype[n_rows][channels], grad_sum_stride, or NULL (zeros).
  *   d_h          h as tc_rms_norm left it (x where there is no residual), h_stride.
