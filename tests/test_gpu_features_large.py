@@ -62,6 +62,9 @@ CONV = [  # tiles of 256 rows: many rows, or more than 64 output channels
     (98500, 1, 7, 9, BF16, 0), (98500, 9, 48, 64, F32, 16), (98500, 2, 200, 48, BF16, 0),
     (33000, 27, 128, 96, BF16, 0), (33000, 5, 100, 128, BF16, 0), (33000, 5, 128, 128, F32, 5), (33000, 4, 200, 70, F16, 0),
     (33000, 3, 256, 72, BF16, 0), (33000, 40, 32, 65, BF16, 0), (33000, 6, 60, 100, F32, 0), (17000, 3, 64, 200, BF16, 0),
+    # tiles of 256 rows from any address, with the weights of all taps in LDS and without
+    (98500, 8, 120, 64, F32, 3), (98500, 8, 52, 45, F16, 4), (98500, 27, 60, 60, F16, 0), (98500, 27, 52, 20, BF16, 0),
+    (98500, 9, 100, 60, BF16, 0), (98500, 27, 100, 12, F32, 0), (98500, 32, 10, 16, BF16, 0),
     # tiles of 64 rows
     (8300, 27, 64, 64, BF16, 0), (8300, 8, 100, 33, F16, 0), (8300, 33, 12, 16, F32, 0), (8300, 3, 200, 40, BF16, 0),
     (8300, 2, 5, 7, BF16, 0), (4200, 27, 96, 100, BF16, 0), (8300, 1, 128, 20, F32, 3), (8300, 5, 8, 32, BF16, 0)]

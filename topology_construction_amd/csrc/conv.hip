@@ -73,6 +73,26 @@ struct Channels {
   }
 };
 
+// The place of row `tid` of a tile in the order of its rows: the Gray rank of its taps' mask,
+// a bit a tap, then its number (below 256).
+__device__ __forceinline__ uint32_t order_key(uint32_t mask, int taps, int tid) {
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) mask ^= mask >> d;
+  mask <<= taps < 32 ? 32 - taps : 0;
+  return (mask & ~255u) | tid;
+}
+template <int BM>
+__device__ __forceinline__ int rank_of(const uint32_t* s_key, int tid) {
+  const uint32_t mine = s_key[tid];
+  int rank = 0;
+#pragma unroll 8
+  for (int i = 0; i < BM; i += 4) {
+    const uint4 o = *reinterpret_cast<const uint4*>(s_key + i);
+    rank += (o.x < mine) + (o.y < mine) + (o.z < mine) + (o.w < mine);
+  }
+  return rank;
+}
+
 // One workgroup of four waves per 64 kRows output rows and 16 kCols output
 // channels; a wave has kRows groups of 16 rows.
 //
@@ -130,23 +150,10 @@ __global__ void __launch_bounds__(kConvWaves * 64, kWide ? 1 : 2) k_conv_tile(Pr
       for (int b = 0; b < 32; ++b)
         if (b * every < taps) mask |= has(m[b * every]) << b;
     }
-    if (row0 + tid >= a.rows) mask = 0;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) mask ^= mask >> d;
-    mask <<= taps < 32 ? 32 - taps : 0;
-    s_key[tid] = (mask & ~255u) | tid;
+    s_key[tid] = order_key(row0 + tid < a.rows ? mask : 0, taps, tid);
   }
   __syncthreads();
-  if (tid < BM) {
-    const uint32_t mine = s_key[tid];
-    int rank = 0;
-#pragma unroll 8
-    for (int i = 0; i < BM; i += 4) {
-      const uint4 o = *reinterpret_cast<const uint4*>(s_key + i);
-      rank += (o.x < mine) + (o.y < mine) + (o.z < mine) + (o.w < mine);
-    }
-    s_order[rank] = tid;
-  }
+  if (tid < BM) s_order[rank_of<BM>(s_key, tid)] = tid;
   __syncthreads();
 
   // a lane's own row (of its group's 16): it holds the row's map entries and scale
@@ -352,6 +359,134 @@ __global__ void __launch_bounds__(kConvWaves * 64, kWide ? 1 : 2) k_conv_tile(Pr
     const Channels<kPair * 4> out(a, n0 + t * 16 + lc * 4 * kPair);
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
+      const i64 row = row0 + s_order[(j * kConvWaves + wave) * 16 + lr];
+      if (row >= a.rows) continue;
+      float v[kPair * 4];
+#pragma unroll
+      for (int i = 0; i < kPair * 4; ++i) v[i] = acc[j][t + i / 4][i % 4];
+      out.store(a, row, v);
+    }
+  }
+}
+
+// Few weights: those of all taps stay in LDS, beside the map entries of the workgroup's
+// 256 rows. The rows are sorted by their masks as in k_conv_tile; then every wave goes
+// through the taps of its four groups by itself, without a barrier, one tap of each group under way
+// at a time, rows straight from memory as matrix operands (from any address).
+template <int kCols, int kSteps>
+__global__ void __launch_bounds__(kConvWaves * 64, 2) k_conv_resident(ProductArgs a) {
+  constexpr int BM = kConvWaves * 64, BN = kCols * 16, kGroups = 4;
+  extern __shared__ __align__(16) int8_t s_dynamic[];  // weights, then entries [BM][taps | 1]
+  __shared__ __align__(16) uint32_t s_key[BM];
+  __shared__ uint32_t s_mask[BM];
+  __shared__ int s_order[BM];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lc = lane >> 4;
+  const i64 row0 = xcd_block(blockIdx.x, gridDim.x) * BM;
+  const int taps = a.taps, k = a.k, pitch = taps | 1, parts = taps * kSteps * kCols;
+  int32_t* const s_map = reinterpret_cast<int32_t*>(s_dynamic + parts * 1024);
+
+  {
+    uint32_t mask = 0;
+    const bool live = row0 + tid < a.rows;
+    const int32_t* m = a.map + min(row0 + tid, a.rows - 1) * taps;
+    int32_t* const mine = s_map + tid * pitch;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i * 4 >= taps) break;
+      const int first = taps >= 4 ? min(i * 4, taps - 4) : 0;
+      v4i e;
+      if (taps >= 4) {
+        __builtin_memcpy(&e, m + first, 16);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) e[u] = m[min(u, taps - 1)];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (first + u >= taps) continue;
+        const bool has = live && (uint32_t)e[u] < (uint32_t)a.n_src;
+        mine[first + u] = has ? e[u] : -1;
+        mask |= (uint32_t)has << (first + u);
+      }
+    }
+    s_mask[tid] = mask;
+    s_key[tid] = order_key(mask, taps, tid);
+  }
+  const int load_row = lane >> 2;
+#pragma unroll 4
+  for (int part = wave; part < parts; part += kConvWaves) {
+    const int r = part % kCols * 16 + load_row;
+    const int c = part / kCols % kSteps * 64 + ((lane & 3) ^ weight_key<kCols>(r)) * 16;
+    const int8_t* from = a.w + ((i64)(part / (kCols * kSteps)) * a.n + min(r, a.n - 1)) * k;
+    *reinterpret_cast<v4i*>(s_dynamic + part * 1024 + lane * 16) =
+        k >= 16 ? weight_16_end(from, c, k) : load_16_tail(from, c, k);
+  }
+  __syncthreads();
+  s_order[rank_of<BM>(s_key, tid)] = tid;
+  __syncthreads();
+
+  // group j of this wave: rows (4 j + wave) * 16 on of that order
+  uint32_t own = s_mask[s_order[(lc * kConvWaves + wave) * 16 + lr]];
+  own = lanes_reduce<16>(own, [](uint32_t x, uint32_t y) { return x | y; });
+  uint32_t left[kGroups];
+  const int32_t* entries[kGroups];
+#pragma unroll
+  for (int j = 0; j < kGroups; ++j) {
+    left[j] = __builtin_amdgcn_readlane(own, j * 16);
+    entries[j] = s_map + s_order[(j * kConvWaves + wave) * 16 + lr] * pitch;
+  }
+  v4i x[kGroups][kSteps];
+  float xs[kGroups];
+  int at[kGroups];  // the tap under way, -1: none
+  auto ask = [&](int j) {
+    at[j] = left[j] ? __builtin_ctz(left[j]) : -1;
+    if (at[j] < 0) return;
+    left[j] &= left[j] - 1;
+    const int e = entries[j][at[j]];
+    const int8_t* from = a.x + max(e, 0) * a.x_stride;  // any row where there is none: its scale is zero
+    xs[j] = e >= 0 ? a.x_scale[e] : 0.0f;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+      x[j][s] = k >= 16 ? load_16_end(from, s * 64 + lc * 16, k) : load_16_tail(from, s * 64 + lc * 16, k);
+  };
+  v4f acc[kGroups][kCols];
+#pragma unroll
+  for (int j = 0; j < kGroups; ++j) {
+    ask(j);
+#pragma unroll
+    for (int t = 0; t < kCols; ++t) acc[j][t] = v4f{0, 0, 0, 0};
+  }
+  while (max(max(at[0], at[1]), max(at[2], at[3])) >= 0) {
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) {
+      if (at[j] < 0) continue;
+      const int8_t* tile = s_dynamic + at[j] * (kSteps * kCols * 1024);
+      v4i d[kCols];
+#pragma unroll
+      for (int t = 0; t < kCols; ++t) {
+        const int r = weight_row<kCols>(t, lr);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          const v4i w = *reinterpret_cast<const v4i*>(tile + (s * BN + r) * 64 + ((lc ^ weight_key<kCols>(r)) * 16));
+          d[t] = product_16(w, x[j][s], s == 0 ? v4i{0, 0, 0, 0} : d[t]);
+        }
+      }
+      const float scale = xs[j];
+      ask(j);
+#pragma unroll
+      for (int t = 0; t < kCols; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[j][t][i] += scale * (float)d[t][i];
+    }
+  }
+
+  constexpr int kPair = kCols < 2 ? 1 : 2;
+#pragma unroll
+  for (int t = 0; t < kCols; t += kPair) {
+    const Channels<kPair * 4> out(a, t * 16 + lc * 4 * kPair);
+#pragma unroll
+    for (int j = 0; j < kGroups; ++j) {
       const i64 row = row0 + s_order[(j * kConvWaves + wave) * 16 + lr];
       if (row >= a.rows) continue;
       float v[kPair * 4];
@@ -605,6 +740,26 @@ void conv_few(const ProductArgs& a, hipStream_t s) {
   launch("k_conv_few", k_conv_few<kCols>, ceil_div(a.rows, 16) * tn, kFewWaves * 64, s, a, tn);
 }
 
+// LDS of k_conv_resident; 0 where it does not take the call.
+int resident_lds(const ProductArgs& a, int cols) {
+  if (a.taps > 32 || a.k > 128 || a.n > 128) return 0;
+  const int lds = a.taps * cols * (a.k > 64 ? 2 : 1) * 1024 + kConvWaves * 64 * (a.taps | 1) * 4;
+  return lds <= 76 * 1024 ? lds : 0;  // two workgroups a CU, with 3 KiB of their own
+}
+template <int kCols>
+void conv_resident(const ProductArgs& a, hipStream_t s) {
+  const i64 blocks = ceil_div(a.rows, kConvWaves * 64);
+  const size_t lds = resident_lds(a, kCols);
+  auto run = [&](auto kernel) {
+    // beyond 64 KiB the kernel has to be told
+    if (lds > 60 * 1024) hip_check(hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                  76 * 1024), "hipFuncSetAttribute");
+    launch_lds("k_conv_resident", kernel, blocks, kConvWaves * 64, lds, s, a);
+  };
+  if (a.k > 64) run(k_conv_resident<kCols, 2>);
+  else run(k_conv_resident<kCols, 1>);
+}
+
 // Calls f<kCols> for the channels of a tile.
 template <typename F>
 void with_cols(int n, F&& f) {
@@ -629,7 +784,11 @@ void with_cols(int n, F&& f) {
 //   2.7k    60 -> 60               19   12
 // A tile of 256 rows reads its weights for four times the rows and skips more, and needs
 // about one workgroup a CU to be worth it; where it has 64 channels or fewer to share a row
-// among, more. Taps split over waves win while the rows leave CUs idle.
+// among, more. Taps split over waves win while the rows leave CUs idle. Of the tiles, those
+// with the weights of all taps in LDS are faster where rows would come through registers
+// anyway (52 -> 45 onto 108k refined voxels 16 us for 21, 60 -> 60 onto 522k 46 for 72, from 110k to
+// half the resolution 28 for 45, 27 taps 12 -> 12 40 for 51), and slower on most aligned ones (64 -> 64
+// to half the resolution 26 for 20, 27 taps 16 -> 16 31 for 29; 32 -> 16 onto 522k 21 for 27).
 void conv_i8(const ProductArgs& a, hipStream_t s) {
   const i64 cus = device_cu_count();
   auto tiles = [&](int rows, int cols) { return ceil_div(a.rows, rows) * ceil_div(a.n, cols); };
@@ -637,7 +796,10 @@ void conv_i8(const ProductArgs& a, hipStream_t s) {
   const bool direct = (((uintptr_t)a.x | (uintptr_t)a.x_stride | (uintptr_t)a.w | (uintptr_t)a.k) & 15) == 0 &&
                       a.n_src * a.x_stride + a.k < (1ll << 31);
   if (2 * tiles(256, 128) >= (a.n > 64 ? cus : 3 * cus))
-    return with_cols(a.n, [&](auto c) { conv_tile<decltype(c)::value>(a, direct, s); });
+    return with_cols(a.n, [&](auto c) {
+      if (!direct && resident_lds(a, decltype(c)::value)) conv_resident<decltype(c)::value>(a, s);
+      else conv_tile<decltype(c)::value>(a, direct, s);
+    });
   if (tiles(64, 64) >= cus / 2) return with_cols(a.n, [&](auto c) { conv_mid<std::min(decltype(c)::value, 4)>(a, s); });
   if (tiles(16, 64) >= cus) return conv_few<4>(a, s);
   if (tiles(16, 32) >= cus) return conv_few<2>(a, s);
