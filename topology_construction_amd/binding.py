@@ -5,7 +5,8 @@ module only converts torch tensors to device pointers, passes torch's current
 stream, supplies torch's caching allocator for the output buffers and wraps the
 results as torch tensor views. It never computes topology itself and raises
 when the library is missing. The operators on feature rows (tc_rms_norm,
-tc_matmul_i8, tc_sparse_conv_i8, ...) take and return torch tensors directly.
+tc_matmul_i8, tc_sparse_conv_i8, ...) take and return torch tensors directly,
+through ``_features.so`` (csrc/bind.cpp).
 
 Function names follow the C ABI (tc_batch_from_ijk, tc_build_batched_topology,
 tc_enumerate_ijk, tc_batch_read_headers, ...).
