@@ -379,9 +379,9 @@ tc_status tc_rms_norm_i8(const void* d_x, int64_t x_stride, const void* d_residu
                          float eps, void* d_sum, int8_t* d_q, float* d_scale, void* stream);
 
 /* Gradient of tc_rms_norm. With dy the gradient of out, dh that of h by its other
- * uses (the residual stream) and g = dy w:
- *   grad_x = s g - h s^3 mean(g h) + dh, rounded to dtype: the gradient of x, and of r alike;
- *   grad_weight = sum over rows of dy h s, a 32-bit float sum in an order that
+ * uses (the residual stream), g = dy w and u = h s:
+ *   grad_x = s (g - u mean(g u)) + dh, rounded to dtype: the gradient of x, and of r alike;
+ *   grad_weight = sum over rows of dy u, a 32-bit float sum in an order that
  *   only n_rows, channels and dtype decide.
  *   d_grad_out   dtype[n_rows][channels], grad_out_stride.
  *   d_grad_sum   dh, dtype[n_rows][channels], grad_sum_stride, or NULL (zeros).
