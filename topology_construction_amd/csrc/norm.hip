@@ -5,8 +5,8 @@
 //
 // h is rounded to the rows' type once and the norm is the norm of that rounded
 // h, so the gradient taken from the stored h is the gradient of what was
-// computed. The mean is a float sum of float squares. Memory bounds all of it:
-// every kernel reads a row once, holds it in registers over its reductions and
+// computed. Squares and their sum are 64-bit: those of finite rows leave 32 bits on either
+// side (from 1.8e19 on, below 1e-19), s and the outputs do not. Memory bounds all of it: every kernel reads a row once, holds it in registers over its reductions and
 // writes once.
 #include "rows.hpp"
 
@@ -88,38 +88,53 @@ __device__ __forceinline__ void load_weights(float (&w)[N][Vec<T>::kN], const Ro
 
 // Sums over the L threads of a group, L a power of two up to a wave, or a workgroup of
 // four waves. Every thread gets the sum, in an order that only L decides.
+template <typename V>
 struct GroupScratch {
-  double d[2][4];
-  float f[2][4];
+  V sum[2][4], top[2][4];
 };
 
-template <int L>
-__device__ __forceinline__ float group_sum(float v, GroupScratch& s, int turn) {
-  v = lanes_reduce<(L < kWave ? L : kWave)>(v, [](float a, float b) { return a + b; });
+template <int L, typename V>
+__device__ __forceinline__ V group_sum(V v, GroupScratch<V>& s, int turn) {
+  v = lanes_reduce<(L < kWave ? L : kWave)>(v, [](V a, V b) { return a + b; });
   if constexpr (L > kWave) {
-    if ((threadIdx.x & (kWave - 1)) == 0) s.f[turn][threadIdx.x / kWave] = v;
+    if ((threadIdx.x & (kWave - 1)) == 0) s.sum[turn][threadIdx.x / kWave] = v;
     __syncthreads();
-    v = (s.f[turn][0] + s.f[turn][1]) + (s.f[turn][2] + s.f[turn][3]);
+    v = (s.sum[turn][0] + s.sum[turn][1]) + (s.sum[turn][2] + s.sum[turn][3]);
   }
   return v;
 }
 
 // As group_sum, with the largest `top` beside the sum.
 template <int L>
-__device__ __forceinline__ void group_sum_max(float& v, double& top, GroupScratch& s, int turn) {
+__device__ __forceinline__ void group_sum_max(double& v, double& top, GroupScratch<double>& s, int turn) {
   constexpr int W = L < kWave ? L : kWave;
-  v = lanes_reduce<W>(v, [](float a, float b) { return a + b; });
+  v = lanes_reduce<W>(v, [](double a, double b) { return a + b; });
   top = lanes_reduce<W>(top, [](double a, double b) { return fmax(a, b); });
   if constexpr (L > kWave) {
     if ((threadIdx.x & (kWave - 1)) == 0) {
-      s.f[turn][threadIdx.x / kWave] = v;
-      s.d[turn][threadIdx.x / kWave] = top;
+      s.sum[turn][threadIdx.x / kWave] = v;
+      s.top[turn][threadIdx.x / kWave] = top;
     }
     __syncthreads();
-    v = (s.f[turn][0] + s.f[turn][1]) + (s.f[turn][2] + s.f[turn][3]);
-    top = fmax(fmax(s.d[turn][0], s.d[turn][1]), fmax(s.d[turn][2], s.d[turn][3]));
+    v = (s.sum[turn][0] + s.sum[turn][1]) + (s.sum[turn][2] + s.sum[turn][3]);
+    top = fmax(fmax(s.top[turn][0], s.top[turn][1]), fmax(s.top[turn][2], s.top[turn][3]));
   }
 }
+
+// s = root * 2^shift from the mean of the squares and eps: the root of a number in [1/2, 2), in
+// 32 bits whatever the range of the row.
+struct InverseRoot {
+  float root;
+  int shift;
+  __device__ __forceinline__ explicit InverseRoot(double mean) {
+    const int half = __builtin_amdgcn_frexp_exp(mean) >> 1;  // 0 for 0, infinity and NaN
+    root = 1.0f / sqrtf((float)ldexp(mean, -2 * half));
+    shift = -half;
+  }
+  // h s: the power first, so that s need not fit 32 bits (rows below 2^-126 with eps = 0)
+  __device__ __forceinline__ float times(float h) const { return ldexpf(h, shift) * root; }
+  __device__ __forceinline__ float value() const { return ldexpf(root, shift); }
+};
 
 // |h w| in 64 bits, where it is exact; infinite for an infinity or NaN.
 __device__ __forceinline__ double magnitude(double p) {
@@ -128,9 +143,9 @@ __device__ __forceinline__ double magnitude(double p) {
 }
 
 // The factor of the row's 8-bit values, and its scale.
-__device__ __forceinline__ double row_factor(double top, float rstd, float& scale) {
+__device__ __forceinline__ double row_factor(double top, const InverseRoot& s, float& scale) {
   const bool finite = top < INFINITY, some = top > 0.0;
-  scale = finite ? (some ? (float)top * rstd / 127.0f : 0.0f) : NAN;
+  scale = finite ? (some ? (float)ldexp(top * s.root * (1.0 / 127.0), s.shift) : 0.0f) : NAN;
   return finite && some ? 127.0 / top : 0.0;
 }
 
@@ -150,8 +165,9 @@ __device__ __forceinline__ int8_t nearest_i8(double p, double factor) {
 template <typename T, int L, int N, bool kI8>
 __global__ void __launch_bounds__(kNormThreads) k_rms_norm(NormArgs a) {
   constexpr int V = Vec<T>::kN;
-  __shared__ GroupScratch s_red;
+  __shared__ GroupScratch<double> s_red;
   const RowPlace<T, L, N> at(a.channels);
+  const double per_channel = 1.0 / (double)a.channels;
   const i64 step = (i64)gridDim.x * (kNormThreads / L);
   i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L;
   Vec<T> x[N], r[N];  // of the next row, asked for before the row at hand is reduced
@@ -172,21 +188,20 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm(NormArgs a) {
       for (int e = 0; e < V; ++e)
         h[j].v[e] = a.residual ? from_f32<T>(to_f32(x[j].v[e]) + to_f32(r[j].v[e])) : x[j].v[e];
     ask(row + step);
-    float ss = 0.0f;
-    double top = 0.0;
+    double ss = 0.0, top = 0.0;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       if (at.c[j] < 0) continue;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float f = to_f32(h[j].v[e]);
+        const double f = to_f32(h[j].v[e]);
         if (!at.ragged || e >= at.skip[j]) ss += f * f;
-        if constexpr (kI8) top = fmax(top, magnitude((double)f * (double)w[j][e]));
+        if constexpr (kI8) top = fmax(top, magnitude(f * (double)w[j][e]));
       }
     }
     if constexpr (kI8) group_sum_max<L>(ss, top, s_red, turn);
     else ss = group_sum<L>(ss, s_red, turn);
-    const float rstd = 1.0f / sqrtf(ss / (float)a.channels + a.eps);
+    const InverseRoot s(ss * per_channel + (double)a.eps);
     const bool first = threadIdx.x % L == 0;
     if (a.sum) {
       T* sum = static_cast<T*>(a.sum) + row * a.channels;
@@ -196,7 +211,7 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm(NormArgs a) {
     }
     if constexpr (kI8) {
       float scale;
-      const double to_q = row_factor(top, rstd, scale);
+      const double to_q = row_factor(top, s, scale);
       if (first) a.scale[row] = scale;
       int8_t* q = a.q + row * a.channels;
 #pragma unroll
@@ -209,14 +224,14 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm(NormArgs a) {
         __builtin_memcpy(q + at.c[j], b, V);
       }
     } else {
-      if (a.rstd && first) a.rstd[row] = rstd;
+      if (a.rstd && first) a.rstd[row] = s.value();
       T* out = static_cast<T*>(a.out) + row * a.channels;
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         if (at.c[j] < 0) continue;
         Vec<T> o;
 #pragma unroll
-        for (int e = 0; e < V; ++e) o.v[e] = from_f32<T>(to_f32(h[j].v[e]) * rstd * w[j][e]);
+        for (int e = 0; e < V; ++e) o.v[e] = from_f32<T>(s.times(to_f32(h[j].v[e])) * w[j][e]);
         o.store(out + at.c[j]);
       }
     }
@@ -231,7 +246,7 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm(NormArgs a) {
 template <typename T, int L, int N, bool kWeight>
 __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad(NormGradArgs a) {
   constexpr int V = Vec<T>::kN;
-  __shared__ GroupScratch s_red;
+  __shared__ GroupScratch<float> s_red;
   const RowPlace<T, L, N> at(a.channels);
   const i64 step = (i64)gridDim.x * (kNormThreads / L);
   i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L;
@@ -331,7 +346,8 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad(NormGradArgs a) 
 // than a workgroup's registers hold (L = a workgroup, the row read twice).
 template <typename T, int L>
 __global__ void __launch_bounds__(kNormThreads) k_rms_norm_any(NormArgs a) {
-  __shared__ GroupScratch s_red;
+  __shared__ GroupScratch<double> s_red;
+  const double per_channel = 1.0 / (double)a.channels;
   const int g = threadIdx.x % L;
   int turn = 0;
   for (i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L; row < a.rows;
@@ -339,29 +355,28 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_any(NormArgs a) {
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
     const T* r = a.residual ? static_cast<const T*>(a.residual) + row * a.residual_stride : nullptr;
     T* sum = a.sum ? static_cast<T*>(a.sum) + row * a.channels : nullptr;
-    float ss = 0.0f;
-    double top = 0.0;
+    double ss = 0.0, top = 0.0;
     for (int c = g; c < a.channels; c += L) {
       const T h = r ? from_f32<T>(to_f32(x[c]) + to_f32(r[c])) : x[c];
       if (sum) sum[c] = h;
-      const float f = to_f32(h);
+      const double f = to_f32(h);
       ss += f * f;
-      if (a.q) top = fmax(top, magnitude((double)f * (double)weight_at(a.weight, a.weight_dtype, c)));
+      if (a.q) top = fmax(top, magnitude(f * (double)weight_at(a.weight, a.weight_dtype, c)));
     }
     group_sum_max<L>(ss, top, s_red, turn);
-    const float rstd = 1.0f / sqrtf(ss / (float)a.channels + a.eps);
-    if (a.rstd && g == 0) a.rstd[row] = rstd;
+    const InverseRoot s(ss * per_channel + (double)a.eps);
+    if (a.rstd && g == 0) a.rstd[row] = s.value();
     double to_q = 0.0;
     if (a.q) {
       float scale;
-      to_q = row_factor(top, rstd, scale);
+      to_q = row_factor(top, s, scale);
       if (g == 0) a.scale[row] = scale;
     }
     // h where this thread stored it, else x and r again
     for (int c = g; c < a.channels; c += L) {
       const T h = sum ? sum[c] : (r ? from_f32<T>(to_f32(x[c]) + to_f32(r[c])) : x[c]);
       const float f = to_f32(h), w = weight_at(a.weight, a.weight_dtype, c);
-      if (a.out) static_cast<T*>(a.out)[row * a.channels + c] = from_f32<T>(f * rstd * w);
+      if (a.out) static_cast<T*>(a.out)[row * a.channels + c] = from_f32<T>(s.times(f) * w);
       if (a.q) a.q[row * a.channels + c] = to_q > 0.0 ? nearest_i8((double)f * (double)w, to_q) : 0;
     }
   }
@@ -369,7 +384,7 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_any(NormArgs a) {
 
 template <typename T, int L>
 __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad_any(NormGradArgs a) {
-  __shared__ GroupScratch s_red;
+  __shared__ GroupScratch<float> s_red;
   const int g = threadIdx.x % L;
   int turn = 0;
   for (i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L; row < a.rows;
