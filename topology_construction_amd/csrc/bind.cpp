@@ -65,14 +65,14 @@ struct Matrix {
   void* p = nullptr;
   int64_t stride = 0, rows = 0, cols = 0;
 };
-// A device matrix with unit channel stride, any row stride; rows or cols of -1 may be any.
+// A device matrix with unit channel stride (any strides where it has no rows), any row stride; rows or cols of -1 may be any.
 Matrix matrix(const Tensor& t, const char* name, at::ScalarType dtype, int device, int64_t rows = -1,
               int64_t cols = -1) {
   check_kind(t, name, dtype, device);
   if (t.dim() != 2 || (rows >= 0 && t.size(0) != rows) || (cols >= 0 && t.size(1) != cols))
     bad_value(std::string(name) + " has the wrong shape: expected [" + (rows < 0 ? "rows" : std::to_string(rows)) +
               ", " + (cols < 0 ? "channels" : std::to_string(cols)) + "]");
-  if (t.stride(1) != 1 && t.size(1) > 1) bad_value(std::string(name) + " must have unit channel stride");
+  if (t.stride(1) != 1 && t.size(1) > 1 && t.size(0) > 0) bad_value(std::string(name) + " must have unit channel stride");
   return {t.data_ptr(), t.stride(0), t.size(0), t.size(1)};
 }
 
