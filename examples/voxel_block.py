@@ -6,7 +6,7 @@ enumeration; a 3x3x3 kernel map of the batch onto itself says what a convolution
 Serving, in 8 bits:   norm -> 3x3x3 convolution -> norm with the residual's addition ->
                       widening projection -> activation -> norm -> narrowing projection,
                       then a transposed 2x2x2 convolution onto the refined grids.
-Training, one norm:   the norm with the residual's addition as an autograd function.
+Training, one norm:   the norm with the residual's addition, recorded by autograd.
 
 Run:  python examples/voxel_block.py [--workload 2] [--channels 128]
 """
@@ -22,21 +22,13 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 from topology_construction_amd import binding, synth  # noqa: E402
 
 
-class RmsNorm(torch.autograd.Function):
-    """(out, h) of tc_rms_norm, differentiable in x, residual and weight."""
+class RmsNorm:
+    """The training form: (out, h), recorded by autograd in x, residual and weight."""
 
     @staticmethod
-    def forward(ctx, x, residual, weight):
-        out, h, rstd = binding.tc_rms_norm(x, weight, residual=residual)
-        ctx.save_for_backward(h, weight, rstd)
+    def apply(x, residual, weight):
+        out, h, _ = binding.tc_rms_norm(x, weight, residual=residual)
         return out, h
-
-    @staticmethod
-    def backward(ctx, grad_out, grad_h):
-        h, weight, rstd = ctx.saved_tensors
-        grad, grad_weight = binding.tc_rms_norm_backward(grad_out.contiguous(), h, weight, rstd,
-                                                         grad_h=grad_h.contiguous())
-        return grad, grad, grad_weight.to(weight.dtype)
 
 
 def quantise_weights(w):

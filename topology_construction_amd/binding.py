@@ -535,6 +535,8 @@ class _Ops:
         self.device = getattr(torch._C, "_cuda_getDevice") if torch.cuda.is_available() else lambda: -1
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         self.stream = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
+        self.records = f.records
+        self.norm_function = _norm_function(self)
 
     def call(self, f, stream, *args):
         """f on the current stream, or on `stream`: outputs are taken on the stream they are written on."""
@@ -543,6 +545,42 @@ class _Ops:
             return f(*args, device, self.stream(device) if device >= 0 else 0)
         with self.on_stream(stream):
             return f(*args, device, stream.cuda_stream)
+
+
+def _norm_function(ops):
+    """tc_rms_norm as an autograd function; its backward is tc_rms_norm_backward."""
+    import torch
+
+    def rows(grad):  # a gradient may come with any strides
+        return grad if grad.stride(1) == 1 or grad.shape[1] == 1 else grad.contiguous()
+
+    class RmsNorm(torch.autograd.Function):
+        """(out, rstd), and h between them where there is a residual: without one h is x itself,
+        whose other uses autograd adds up by itself."""
+
+        @staticmethod
+        def forward(ctx, x, weight, residual, eps):
+            out, h, rstd = ops.call(ops.rms_norm, None, x, weight, residual, eps)
+            ctx.save_for_backward(h, weight, rstd)
+            ctx.set_materialize_grads(False)
+            ctx.mark_non_differentiable(rstd)
+            return (out, rstd) if residual is None else (out, h, rstd)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, grad_out, *grad_rest):
+            h, weight, rstd = ctx.saved_tensors
+            grad_h = grad_rest[0] if len(grad_rest) == 2 else None
+            grad, grad_weight = grad_h, None
+            if grad_out is not None:
+                grad, grad_weight = ops.call(ops.rms_norm_backward, None, rows(grad_out), h, weight, rstd,
+                                             None if grad_h is None else rows(grad_h))
+                if weight is not None:
+                    grad_weight = grad_weight.to(weight.dtype)
+            needs = ctx.needs_input_grad
+            return grad if needs[0] else None, grad_weight if needs[1] else None, grad if needs[2] else None, None
+
+    return RmsNorm.apply
 
 
 _ops_state = None
@@ -558,14 +596,22 @@ def _ops() -> _Ops:
 def tc_rms_norm(x, weight=None, residual=None, eps: float = 1e-6, stream=None):
     """Root-mean-square norm of rows: h = x + residual, s = 1 / sqrt(mean(h^2) + eps),
     out = h * s * weight. Returns (out, h, rstd): h is x itself without a residual,
-    rstd float32 [rows] is s, kept for tc_rms_norm_backward."""
+    rstd float32 [rows] is s, kept for tc_rms_norm_backward. Where autograd records (x, weight
+    or residual requires a gradient), out and h carry the graph; rstd never does, and there
+    are no second derivatives and no forward-mode tangents. The other operators here record nothing."""
     ops = _ops()
+    if ops.records(x, weight, residual):
+        if stream is not None:  # the backward runs on the stream that the forward was recorded on
+            with ops.on_stream(stream):
+                return tc_rms_norm(x, weight, residual, eps)
+        r = ops.norm_function(x, weight, residual, eps)
+        return r if residual is not None else (r[0], x, r[1])
     return ops.call(ops.rms_norm, stream, x, weight, residual, eps)
 
 
 def tc_rms_norm_i8(x, weight=None, residual=None, eps: float = 1e-6, stream=None):
     """The norm with an 8-bit output: (q int8 [rows, channels], scale float32 [rows], h),
-    q * scale standing for h * s * weight."""
+    q * scale standing for h * s * weight. Nothing is recorded for a gradient."""
     ops = _ops()
     return ops.call(ops.rms_norm_i8, stream, x, weight, residual, eps)
 

@@ -5,6 +5,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -317,6 +318,18 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
   return nullptr;
 }
 
+// Whether autograd records a call on these (what is no tensor is passed over): it is on and one
+// requires a gradient, or one has a forward-mode tangent.
+PyObject* records(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  const bool on = c10::GradMode::is_enabled();
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    if (!THPVariable_Check(args[i])) continue;
+    const Tensor& t = THPVariable_Unpack(args[i]);
+    if ((on && t.requires_grad()) || t._fw_grad(0).defined()) Py_RETURN_TRUE;
+  }
+  Py_RETURN_FALSE;
+}
+
 PyObject* set_error(PyObject*, PyObject* type) {
   Py_INCREF(type);
   Py_XSETREF(g_topo_error, type);
@@ -333,6 +346,8 @@ PyMethodDef g_methods[] = {method<rms_norm<false>, 4>("rms_norm"),
                            method<rms_norm_backward, 5>("rms_norm_backward"),
                            method<matmul_i8, 7>("matmul_i8"),
                            method<sparse_conv_i8, 8>("sparse_conv_i8"),
+                           {"records", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&records)),
+                            METH_FASTCALL, nullptr},
                            {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_features", nullptr, -1, g_methods};
