@@ -250,13 +250,20 @@ ProductOut product_out(const ProductIn& p, PyObject* out, PyObject* out_dtype, i
     return o;
   }
   const Tensor& t = tensor(out, "out");
+  if (c10::GradMode::is_enabled() && t.requires_grad()) bad_value("out requires a gradient, which this call has none for");
   o.dt = dtype_id(t.scalar_type());
   o.m = matrix(t, "out", t.scalar_type(), p.device, rows, cols);
   if (o.m.stride < cols && rows > 1) bad_value("the rows of out overlap");
   o.m.stride = std::max(o.m.stride, cols);
   return o;
 }
-PyObject* result(const ProductOut& o, PyObject* out) { return o.made ? THPVariable_Wrap(*o.made) : Py_NewRef(out); }
+PyObject* result(const ProductOut& o, PyObject* out) {
+  if (o.made) return THPVariable_Wrap(*o.made);
+  // autograd sees that the caller's tensor was written
+  const Tensor& t = THPVariable_Unpack(out);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  return Py_NewRef(out);
+}
 
 // (x, x_scale, w, w_scale, bias, out_dtype, out) -> out
 PyObject* matmul_i8(const Args& g) {
