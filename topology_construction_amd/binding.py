@@ -627,7 +627,8 @@ def tc_rms_norm_backward(grad_out, h, weight, rstd, grad_h=None, stream=None):
 def tc_matmul_i8(x, x_scale, w, w_scale, bias=None, out_dtype=None, out=None, stream=None):
     """Product of int8 rows x [rows, c_in] with int8 weights w [c_out, c_in], float32
     scales for each row and each output channel, float32 bias [c_out]: [rows, c_out]
-    of `out_dtype` (bfloat16 unless given), or into `out` (any row stride, and no gradient required)."""
+    of `out_dtype` (bfloat16 unless given), or into `out` (any row stride, and no gradient required;
+    `out_dtype` beside it has to be its own)."""
     ops = _ops()
     return ops.call(ops.matmul_i8, stream, x, x_scale, w, w_scale, bias, out_dtype, out)
 

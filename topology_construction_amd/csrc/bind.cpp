@@ -238,12 +238,12 @@ struct ProductOut {
 };
 ProductOut product_out(const ProductIn& p, PyObject* out, PyObject* out_dtype, int64_t rows, int64_t cols) {
   ProductOut o;
+  auto type = at::kBFloat16;
+  if (out_dtype != Py_None) {
+    if (!THPDtype_Check(out_dtype)) bad_type("out_dtype must be a torch dtype");
+    type = reinterpret_cast<THPDtype*>(out_dtype)->scalar_type;
+  }
   if (out == Py_None) {
-    auto type = at::kBFloat16;
-    if (out_dtype != Py_None) {
-      if (!THPDtype_Check(out_dtype)) bad_type("out_dtype must be a torch dtype");
-      type = reinterpret_cast<THPDtype*>(out_dtype)->scalar_type;
-    }
     o.dt = dtype_id(type);
     o.made = empty(*p.x, {rows, cols}, type);
     o.m = {o.made->data_ptr(), cols, rows, cols};
@@ -251,6 +251,7 @@ ProductOut product_out(const ProductIn& p, PyObject* out, PyObject* out_dtype, i
   }
   const Tensor& t = tensor(out, "out");
   if (c10::GradMode::is_enabled() && t.requires_grad()) bad_value("out requires a gradient, which this call has none for");
+  if (out_dtype != Py_None && type != t.scalar_type()) bad_value("out is of another type than out_dtype");
   o.dt = dtype_id(t.scalar_type());
   o.m = matrix(t, "out", t.scalar_type(), p.device, rows, cols);
   if (o.m.stride < cols && rows > 1) bad_value("the rows of out overlap");
