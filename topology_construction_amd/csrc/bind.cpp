@@ -7,6 +7,7 @@
 #include <ATen/ATen.h>
 #include <c10/core/GradMode.h>
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <optional>
@@ -320,8 +321,8 @@ PyObject* call(PyObject*, PyObject* const* args, Py_ssize_t n) {
     PyObject* a = Py_BuildValue("(is)", e.status, tc_last_error());
     if (a) PyErr_SetObject(g_topo_error, a);
     Py_XDECREF(a);
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (...) {  // torch's own errors as its operators raise them (no memory for an output: OutOfMemoryError)
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }
