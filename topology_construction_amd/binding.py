@@ -539,12 +539,12 @@ class _Ops:
         self.norm_function = _norm_function(self)
 
     def call(self, f, stream, *args):
-        """f on the current stream, or on `stream`: outputs are taken on the stream they are written on."""
-        device = self.device()
+        """f on the current stream, or on `stream` and its device: outputs are taken on the stream they are written on."""
         if stream is None:
+            device = self.device()
             return f(*args, device, self.stream(device) if device >= 0 else 0)
         with self.on_stream(stream):
-            return f(*args, device, stream.cuda_stream)
+            return f(*args, self.device(), stream.cuda_stream)
 
 
 def _norm_function(ops):
