@@ -1,5 +1,5 @@
 // Feature rows: element types, conversions and wave reductions shared by the
-// operators on voxel rows (norm.hip, product.hip).
+// operators on voxel rows (norm.hip, int8.hpp).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -60,6 +60,5 @@ inline void with_dtype(int dtype, F&& f) {
     default: throw Error(TC_ERR_INVALID_ARG, "unknown dtype");
   }
 }
-inline size_t dtype_bytes(int dtype) { return dtype == TC_F32 ? 4 : 2; }
 
 }  // namespace tc
