@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad(NormGradArgs a) 
 
 // Rows of fewer channels than a vector has (L = 1: one thread a row), or of more
 // than a workgroup's registers hold (L = a workgroup, the row read twice).
-template <typename T, int L>
+template <typename T, int L, bool kI8>
 __global__ void __launch_bounds__(kNormThreads) k_rms_norm_any(NormArgs a) {
   __shared__ GroupScratch<double> s_red;
   const double per_channel = 1.0 / (double)a.channels;
@@ -361,13 +361,14 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_any(NormArgs a) {
       if (sum) sum[c] = h;
       const double f = to_f32(h);
       ss += f * f;
-      if (a.q) top = fmax(top, magnitude(f * (double)weight_at(a.weight, a.weight_dtype, c)));
+      if constexpr (kI8) top = fmax(top, magnitude(f * (double)weight_at(a.weight, a.weight_dtype, c)));
     }
-    group_sum_max<L>(ss, top, s_red, turn);
+    if constexpr (kI8) group_sum_max<L>(ss, top, s_red, turn);
+    else ss = group_sum<L>(ss, s_red, turn);
     const InverseRoot s(ss * per_channel + (double)a.eps);
-    if (a.rstd && g == 0) a.rstd[row] = s.value();
+    if (!kI8 && a.rstd && g == 0) a.rstd[row] = s.value();
     double to_q = 0.0;
-    if (a.q) {
+    if constexpr (kI8) {
       float scale;
       to_q = row_factor(top, s, scale);
       if (g == 0) a.scale[row] = scale;
@@ -376,8 +377,8 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_any(NormArgs a) {
     for (int c = g; c < a.channels; c += L) {
       const T h = sum ? sum[c] : (r ? from_f32<T>(to_f32(x[c]) + to_f32(r[c])) : x[c]);
       const float f = to_f32(h), w = weight_at(a.weight, a.weight_dtype, c);
-      if (a.out) static_cast<T*>(a.out)[row * a.channels + c] = from_f32<T>(s.times(f) * w);
-      if (a.q) a.q[row * a.channels + c] = to_q > 0.0 ? nearest_i8((double)f * (double)w, to_q) : 0;
+      if constexpr (kI8) a.q[row * a.channels + c] = to_q > 0.0 ? nearest_i8((double)f * (double)w, to_q) : 0;
+      else static_cast<T*>(a.out)[row * a.channels + c] = from_f32<T>(s.times(f) * w);
     }
   }
 }
@@ -483,13 +484,18 @@ void rms_norm(const NormArgs& a, hipStream_t s) {
     using T = decltype(t);
     constexpr int V = Vec<T>::kN;
     auto blocks = [&](int rows) { return std::min<i64>(ceil_div(a.rows, rows), most); };
-    if (a.channels < V) return launch("k_rms_norm_any", k_rms_norm_any<T, 1>, blocks(kNormThreads), kNormThreads, s, a);
+    auto any = [&](auto l) {
+      constexpr int L = decltype(l)::value;
+      launch("k_rms_norm_any", a.q ? k_rms_norm_any<T, L, true> : k_rms_norm_any<T, L, false>, blocks(kNormThreads / L),
+             kNormThreads, s, a);
+    };
+    if (a.channels < V) return any(std::integral_constant<int, 1>());
     const bool held = with_place(ceil_div(a.channels, V), [&](auto l, auto n) {
       constexpr int L = decltype(l)::value, N = decltype(n)::value;
       if (a.q) launch("k_rms_norm", k_rms_norm<T, L, N, true>, blocks(kNormThreads / L), kNormThreads, s, a);
       else launch("k_rms_norm", k_rms_norm<T, L, N, false>, blocks(kNormThreads / L), kNormThreads, s, a);
     });
-    if (!held) launch("k_rms_norm_any", k_rms_norm_any<T, kNormThreads>, blocks(1), kNormThreads, s, a);
+    if (!held) any(std::integral_constant<int, kNormThreads>());
   });
 }
 
