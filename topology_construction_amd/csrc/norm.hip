@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm(NormArgs a) {
   }
 }
 
-// dx = s (g - u mean(g u)) + dh with g = dy w and the unit row u = h s, and this workgroup's
+// dx = s g - u (s mean(g u)) + dh with g = dy w and the unit row u = h s, and this workgroup's
 // part of dw = sum over rows of dy u: each thread adds up its channels over its rows in
 // registers, the workgroup's groups are joined once at the end. Neither a power of s nor a
 // product with h is formed: those leave 32 bits (rows of 1e14, s^3 = 1e-42) where u does not. 16384 x 4096 f16 114 us
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad(NormGradArgs a) 
     }
     dot = group_sum<L>(dot, s_red, turn);
     if (!a.grad_x) continue;
-    const float along = dot / (float)a.channels;
+    const float along = rstd * (dot / (float)a.channels);
     T* dx = static_cast<T*>(a.grad_x) + row * a.channels;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad(NormGradArgs a) 
       Vec<T> o;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float v = rstd * (to_f32(dy[j].v[e]) * w[j][e] - to_f32(h[j].v[e]) * rstd * along);
+        const float v = rstd * (to_f32(dy[j].v[e]) * w[j][e]) - to_f32(h[j].v[e]) * rstd * along;
         o.v[e] = from_f32<T>(a.grad_sum ? v + to_f32(dh[j].v[e]) : v);
       }
       o.store(dx + at.c[j]);
@@ -398,10 +398,10 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad_any(NormGradArgs
     for (int c = g; c < a.channels; c += L)
       dot += to_f32(dy[c]) * weight_at(a.weight, a.weight_dtype, c) * (to_f32(h[c]) * rstd);
     dot = group_sum<L>(dot, s_red, turn);
-    const float along = dot / (float)a.channels;
+    const float along = rstd * (dot / (float)a.channels);
     for (int c = g; c < a.channels; c += L) {
       const float gy = to_f32(dy[c]) * weight_at(a.weight, a.weight_dtype, c);
-      const float v = rstd * (gy - to_f32(h[c]) * rstd * along);
+      const float v = rstd * gy - to_f32(h[c]) * rstd * along;
       static_cast<T*>(a.grad_x)[row * a.channels + c] = from_f32<T>(dh ? v + to_f32(dh[c]) : v);
     }
   }
