@@ -352,9 +352,10 @@ typedef enum tc_dtype { TC_F32 = 0, TC_F16 = 1, TC_BF16 = 2 } tc_dtype;
 
 /* Root-mean-square norm of every row with the residual's addition (training form):
  *   h = x + r, rounded to dtype; s = 1 / sqrt(mean(h^2) + eps); out = h s w, rounded to dtype.
- * The norm is that of the rounded h. Squares and their sum are 64-bit, so every finite row has
- * its norm; s is a 32-bit float (infinite only where 1 / sqrt(...) leaves its range: rows below
- * 2^-128 with an eps as small, whose out is right all the same).
+ * The norm is that of the rounded h. The sum of the squares is a 32-bit float, or a 64-bit one where
+ * the squares near the ends of 32 bits, so every finite row has its norm; s is a 32-bit float (infinite
+ * only where 1 / sqrt(...) leaves its range: rows below 2^-128 with an eps as small, whose out is right
+ * all the same).
  *   d_x         dtype[n_rows][channels], x_stride.
  *   d_residual  dtype[n_rows][channels], residual_stride, or NULL (h = x).
  *   d_weight    weight_dtype[channels] (TC_F32, or dtype), or NULL (ones).

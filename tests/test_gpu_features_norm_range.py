@@ -13,7 +13,8 @@ WIDTHS = [3, 8, 100, 128, 1000, 2056, 8200, 16392]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("size,eps", [(1e18, 1e-6), (3e19, 1e-6), (1e25, 0.0), (5e37, 1e-6), (1e-18, 0.0), (1e-24, 0.0),
+@pytest.mark.parametrize("size,eps", [(1e18, 1e-6), (3e19, 1e-6), (1e25, 0.0), (5e37, 1e-6), (1e-15, 0.0), (8e-16, 0.0), (2e-16, 1e-32),
+                                      (1e-18, 0.0), (1e-24, 0.0),
                                       (1e-30, 1e-35), (1e-36, 0.0), (1e-39, 0.0)])
 def test_norm_range(size, eps, dtype):
     """5e37: six deviations below the largest value. 1e-39: below the normal range, where s leaves

@@ -5,9 +5,10 @@
 //
 // h is rounded to the rows' type once and the norm is the norm of that rounded
 // h, so the gradient taken from the stored h is the gradient of what was
-// computed. Squares and their sum are 64-bit: those of finite rows leave 32 bits on either
-// side (from 1.8e19 on, below 1e-19), s and the outputs do not. Memory bounds all of it: every kernel reads a row once, holds it in registers over its reductions and
-// writes once.
+// computed. The mean is a float sum of float squares; where that leaves 32 bits or nears the end of
+// their range (rows from 1.8e19 on, or below 1e-15 with an eps as small), the squares are summed
+// again in 64 bits: the norm of a finite row is finite. Memory bounds all of it: every kernel
+// reads a row once, holds it in registers over its reductions and writes once.
 #include "rows.hpp"
 
 namespace tc {
@@ -90,51 +91,57 @@ __device__ __forceinline__ void load_weights(float (&w)[N][Vec<T>::kN], const Ro
 // four waves. Every thread gets the sum, in an order that only L decides.
 template <typename V>
 struct GroupScratch {
-  V sum[2][4], top[2][4];
+  V part[2][4], top[2][4];
 };
 
 template <int L, typename V>
 __device__ __forceinline__ V group_sum(V v, GroupScratch<V>& s, int turn) {
   v = lanes_reduce<(L < kWave ? L : kWave)>(v, [](V a, V b) { return a + b; });
   if constexpr (L > kWave) {
-    if ((threadIdx.x & (kWave - 1)) == 0) s.sum[turn][threadIdx.x / kWave] = v;
+    if ((threadIdx.x & (kWave - 1)) == 0) s.part[turn][threadIdx.x / kWave] = v;
     __syncthreads();
-    v = (s.sum[turn][0] + s.sum[turn][1]) + (s.sum[turn][2] + s.sum[turn][3]);
+    v = (s.part[turn][0] + s.part[turn][1]) + (s.part[turn][2] + s.part[turn][3]);
   }
   return v;
 }
 
 // As group_sum, with the largest `top` beside the sum.
 template <int L>
-__device__ __forceinline__ void group_sum_max(double& v, double& top, GroupScratch<double>& s, int turn) {
+__device__ __forceinline__ void group_sum_max(float& v, double& top, GroupScratch<float>& sums,
+                                              GroupScratch<double>& tops, int turn) {
   constexpr int W = L < kWave ? L : kWave;
-  v = lanes_reduce<W>(v, [](double a, double b) { return a + b; });
+  v = lanes_reduce<W>(v, [](float a, float b) { return a + b; });
   top = lanes_reduce<W>(top, [](double a, double b) { return fmax(a, b); });
   if constexpr (L > kWave) {
     if ((threadIdx.x & (kWave - 1)) == 0) {
-      s.sum[turn][threadIdx.x / kWave] = v;
-      s.top[turn][threadIdx.x / kWave] = top;
+      sums.part[turn][threadIdx.x / kWave] = v;
+      tops.top[turn][threadIdx.x / kWave] = top;
     }
     __syncthreads();
-    v = (s.sum[turn][0] + s.sum[turn][1]) + (s.sum[turn][2] + s.sum[turn][3]);
-    top = fmax(fmax(s.top[turn][0], s.top[turn][1]), fmax(s.top[turn][2], s.top[turn][3]));
+    v = (sums.part[turn][0] + sums.part[turn][1]) + (sums.part[turn][2] + sums.part[turn][3]);
+    top = fmax(fmax(tops.top[turn][0], tops.top[turn][1]), fmax(tops.top[turn][2], tops.top[turn][3]));
   }
 }
 
-// s = root * 2^shift from the mean of the squares and eps: the root of a number in [1/2, 2), in
-// 32 bits whatever the range of the row.
+// s = root * 2^shift: shift is 0 but for rows far from one (above), where it takes the power of
+// two, so that s need not fit 32 bits (rows below 2^-126 with eps = 0).
 struct InverseRoot {
   float root;
   int shift;
-  __device__ __forceinline__ explicit InverseRoot(double mean) {
-    const int half = __builtin_amdgcn_frexp_exp(mean) >> 1;  // 0 for 0, infinity and NaN
-    root = 1.0f / sqrtf((float)ldexp(mean, -2 * half));
-    shift = -half;
-  }
-  // h s: the power first, so that s need not fit 32 bits (rows below 2^-126 with eps = 0)
   __device__ __forceinline__ float times(float h) const { return ldexpf(h, shift) * root; }
   __device__ __forceinline__ float value() const { return ldexpf(root, shift); }
 };
+// Whether the mean of the squares and eps, in 32 bits, is one of a far row: squares below the normal
+// range are off by 2^-150, nothing next to 2^-100. Those of f16 are 2^-48 to 2^32, or zero.
+template <typename T>
+__device__ __forceinline__ bool far(float mean) {
+  return !std::is_same<T, f16>::value && !(mean >= 0x1p-100f && mean < INFINITY);
+}
+// From that mean in 64 bits: the root of a number in [1/2, 2).
+__device__ __forceinline__ InverseRoot far_root(double mean) {
+  const int half = __builtin_amdgcn_frexp_exp(mean) >> 1;  // 0 for 0, infinity and NaN
+  return {1.0f / sqrtf((float)ldexp(mean, -2 * half)), -half};
+}
 
 // |h w| in 64 bits, where it is exact; infinite for an infinity or NaN.
 __device__ __forceinline__ double magnitude(double p) {
@@ -162,12 +169,15 @@ __device__ __forceinline__ int8_t nearest_i8(double p, double factor) {
 // Memory bounds it: 16384 x 4096 f16 91 us (5.9 TB/s), 124800 x 128 bf16 22 us, in 8 bits
 // 124800 x 64 bf16 14 us (4.0 TB/s; products in 32 bits instead of 64 changed nothing), one
 // row of 1024 3.1 us.
+//
+// N = 4: held to the 168 registers of three waves a SIMD (the 8-bit form of 16-bit rows would take a few
+// more: 4096 x 6000 f16 96 us for 92).
 template <typename T, int L, int N, bool kI8>
-__global__ void __launch_bounds__(kNormThreads) k_rms_norm(NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads, N == 4 ? 3 : 1) k_rms_norm(NormArgs a) {
   constexpr int V = Vec<T>::kN;
-  __shared__ GroupScratch<double> s_red;
+  __shared__ GroupScratch<float> s_red;
+  __shared__ GroupScratch<double> s_far;
   const RowPlace<T, L, N> at(a.channels);
-  const double per_channel = 1.0 / (double)a.channels;
   const i64 step = (i64)gridDim.x * (kNormThreads / L);
   i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L;
   Vec<T> x[N], r[N];  // of the next row, asked for before the row at hand is reduced
@@ -188,20 +198,36 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm(NormArgs a) {
       for (int e = 0; e < V; ++e)
         h[j].v[e] = a.residual ? from_f32<T>(to_f32(x[j].v[e]) + to_f32(r[j].v[e])) : x[j].v[e];
     ask(row + step);
-    double ss = 0.0, top = 0.0;
+    float ss = 0.0f;
+    double top = 0.0;
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       if (at.c[j] < 0) continue;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const double f = to_f32(h[j].v[e]);
+        const float f = to_f32(h[j].v[e]);
         if (!at.ragged || e >= at.skip[j]) ss += f * f;
-        if constexpr (kI8) top = fmax(top, magnitude(f * (double)w[j][e]));
+        if constexpr (kI8) top = fmax(top, magnitude((double)f * (double)w[j][e]));
       }
     }
-    if constexpr (kI8) group_sum_max<L>(ss, top, s_red, turn);
+    if constexpr (kI8) group_sum_max<L>(ss, top, s_red, s_far, turn);
     else ss = group_sum<L>(ss, s_red, turn);
-    const InverseRoot s(ss * per_channel + (double)a.eps);
+    const float mean = ss / (float)a.channels + a.eps;
+    InverseRoot s{1.0f / sqrtf(mean), 0};
+    const bool again = far<T>(mean);  // the same for the whole row
+    if (again) {
+      double sum = 0.0;
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        if (at.c[j] < 0) continue;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const double f = to_f32(h[j].v[e]);
+          if (!at.ragged || e >= at.skip[j]) sum += f * f;
+        }
+      }
+      s = far_root(group_sum<L>(sum, s_far, turn) / a.channels + a.eps);
+    }
     const bool first = threadIdx.x % L == 0;
     if (a.sum) {
       T* sum = static_cast<T*>(a.sum) + row * a.channels;
@@ -226,14 +252,18 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm(NormArgs a) {
     } else {
       if (a.rstd && first) a.rstd[row] = s.value();
       T* out = static_cast<T*>(a.out) + row * a.channels;
+      auto write = [&](auto unit) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        if (at.c[j] < 0) continue;
-        Vec<T> o;
+        for (int j = 0; j < N; ++j) {
+          if (at.c[j] < 0) continue;
+          Vec<T> o;
 #pragma unroll
-        for (int e = 0; e < V; ++e) o.v[e] = from_f32<T>(s.times(to_f32(h[j].v[e])) * w[j][e]);
-        o.store(out + at.c[j]);
-      }
+          for (int e = 0; e < V; ++e) o.v[e] = from_f32<T>(unit(to_f32(h[j].v[e])) * w[j][e]);
+          o.store(out + at.c[j]);
+        }
+      };
+      if (again) write([&](float f) { return s.times(f); });
+      else write([&](float f) { return f * s.root; });
     }
   }
 }
@@ -346,8 +376,8 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad(NormGradArgs a) 
 // than a workgroup's registers hold (L = a workgroup, the row read twice).
 template <typename T, int L, bool kI8>
 __global__ void __launch_bounds__(kNormThreads) k_rms_norm_any(NormArgs a) {
-  __shared__ GroupScratch<double> s_red;
-  const double per_channel = 1.0 / (double)a.channels;
+  __shared__ GroupScratch<float> s_red;
+  __shared__ GroupScratch<double> s_far;
   const int g = threadIdx.x % L;
   int turn = 0;
   for (i64 row = (i64)blockIdx.x * (kNormThreads / L) + threadIdx.x / L; row < a.rows;
@@ -355,17 +385,29 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_any(NormArgs a) {
     const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
     const T* r = a.residual ? static_cast<const T*>(a.residual) + row * a.residual_stride : nullptr;
     T* sum = a.sum ? static_cast<T*>(a.sum) + row * a.channels : nullptr;
-    double ss = 0.0, top = 0.0;
+    float ss = 0.0f;
+    double top = 0.0;
     for (int c = g; c < a.channels; c += L) {
       const T h = r ? from_f32<T>(to_f32(x[c]) + to_f32(r[c])) : x[c];
       if (sum) sum[c] = h;
-      const double f = to_f32(h);
+      const float f = to_f32(h);
       ss += f * f;
-      if constexpr (kI8) top = fmax(top, magnitude(f * (double)weight_at(a.weight, a.weight_dtype, c)));
+      if constexpr (kI8) top = fmax(top, magnitude((double)f * (double)weight_at(a.weight, a.weight_dtype, c)));
     }
-    if constexpr (kI8) group_sum_max<L>(ss, top, s_red, turn);
+    if constexpr (kI8) group_sum_max<L>(ss, top, s_red, s_far, turn);
     else ss = group_sum<L>(ss, s_red, turn);
-    const InverseRoot s(ss * per_channel + (double)a.eps);
+    // h where this thread stored it, else x and r again
+    const auto h_at = [&](int c) { return sum ? sum[c] : (r ? from_f32<T>(to_f32(x[c]) + to_f32(r[c])) : x[c]); };
+    const float mean = ss / (float)a.channels + a.eps;
+    InverseRoot s{1.0f / sqrtf(mean), 0};
+    if (far<T>(mean)) {
+      double again = 0.0;
+      for (int c = g; c < a.channels; c += L) {
+        const double f = to_f32(h_at(c));
+        again += f * f;
+      }
+      s = far_root(group_sum<L>(again, s_far, turn) / a.channels + a.eps);
+    }
     if (!kI8 && a.rstd && g == 0) a.rstd[row] = s.value();
     double to_q = 0.0;
     if constexpr (kI8) {
@@ -373,10 +415,8 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_any(NormArgs a) {
       to_q = row_factor(top, s, scale);
       if (g == 0) a.scale[row] = scale;
     }
-    // h where this thread stored it, else x and r again
     for (int c = g; c < a.channels; c += L) {
-      const T h = sum ? sum[c] : (r ? from_f32<T>(to_f32(x[c]) + to_f32(r[c])) : x[c]);
-      const float f = to_f32(h), w = weight_at(a.weight, a.weight_dtype, c);
+      const float f = to_f32(h_at(c)), w = weight_at(a.weight, a.weight_dtype, c);
       if constexpr (kI8) a.q[row * a.channels + c] = to_q > 0.0 ? nearest_i8((double)f * (double)w, to_q) : 0;
       else static_cast<T*>(a.out)[row * a.channels + c] = from_f32<T>(s.times(f) * w);
     }
