@@ -110,11 +110,15 @@ __device__ __forceinline__ int rank_of(const uint32_t* s_key, int tid) {
 // operands before the next stage's are asked for. kDirect: rows and weights on 16-byte
 // boundaries go straight into LDS, otherwise through registers, from any address.
 //
-// 116k rows, 27 taps, 128 -> 128: 69 us, 1.6 us a stage beside 15 for order and stores. Matrix
-// units (0.85 us a stage), LDS and gathers each take about half a stage: what is left
-// is that two workgroups a CU overlap them no better. Sharing the rows among waves that split
-// the channels (balanced skips, but three branches for every 64 products) took 81 us, all
-// groups without branches 78.
+// 116k rows, 27 taps, 128 -> 128: 62 us a call in a row of calls (67 traced alone), 1.8 us a stage beside 14
+// for order, first loads and stores (one tap: 15.5). The matrix units are busy 22% of the cycles, 0.53 us
+// of a stage: what is left is that two workgroups a CU overlap products, LDS and gathers no better. Sharing
+// the rows among waves that split the channels (balanced skips, but three branches for every 64 products)
+// took 81 us where this took 69, all groups without branches 78.
+//
+// kWide keeps integer sums beside the float ones: 309 registers with 64 output channels (358 through
+// registers), one workgroup a CU, and rows gathered again for every 64 channels. 65k rows, 27 taps, 256 -> 256:
+// 310 us for the 46 that its operations take.
 template <int kRows, int kCols, int kSteps, bool kDirect, bool kWide>
 __global__ void __launch_bounds__(kConvWaves * 64, kWide ? 1 : 2) k_conv_tile(ProductArgs a, int tiles_n) {
   constexpr int BM = kConvWaves * kRows * 16, BN = kCols * 16;
@@ -502,6 +506,8 @@ __global__ void __launch_bounds__(kConvWaves * 64, 2) k_conv_resident(ProductArg
 // of a stage (through registers, from any address) are asked for while the stage before is
 // computed; its weights are shared by the waves, in one buffer of LDS. At most 64 output
 // channels: with 128 the registers hold fewer workgroups a CU (14k rows, 100 -> 96: 44 us for 29).
+// Far from what its bytes and operations take (those 29 us: 1.4): of nine stages each has two barriers
+// and one set of loads to wait for, with few waves a CU to fill the wait (read from the code, not measured apart).
 template <int kCols, int kSteps, bool kWide>
 __global__ void __launch_bounds__(kConvWaves * 64, kWide ? 2 : 3) k_conv_mid(ProductArgs a, int tiles_n) {
   constexpr int kTaps = kCols * kSteps > 4 ? 3 : 4;  // of a stage
@@ -782,6 +788,24 @@ void with_cols(int n, F&& f) {
 //   22k     100 -> 96      63      34  100
 //   5.5k    60 -> 96               19   23
 //   2.7k    60 -> 60               19   12
+//   65k     256 -> 256    310     372 1124
+//   22k     256 -> 256   *155     144  390
+//   8.6k    256 -> 256     82     *95  160
+//   8.6k    512 -> 512    270     296  556
+// and over 8-tap maps onto refined (up) and halved (down) grids:
+//   108k up    64 -> 64     15     17    93
+//   69k up     64 -> 64     14     14    58
+//   69k up   128 -> 128     21     35   210
+//   69k up   256 -> 128     64     74   330
+//   22k up   128 -> 128     19     14    67
+//   25k up     60 -> 60     12    9.2    29
+//   8.4k up    64 -> 64     13    7.1    11
+//   82k down   64 -> 64     17     17    76
+//   36k down  64 -> 128    *20     16    68
+//   36k down   64 -> 64     15     10    35
+//   8.9k down 64 -> 128     20    8.3    19
+//   2.4k down 64 -> 128     20    7.1  *8.2
+// The rule takes the fastest, but the starred where there is one: 8 to 29% over the fastest.
 // A tile of 256 rows reads its weights for four times the rows and skips more, and needs
 // about one workgroup a CU to be worth it; where it has 64 channels or fewer to share a row
 // among, more. Taps split over waves win while the rows leave CUs idle. Of the tiles, those

@@ -166,9 +166,9 @@ __device__ __forceinline__ int8_t nearest_i8(double p, double factor) {
 
 // The row stays in registers between the reductions and the outputs. h is stored
 // only after a reduction over the row, when all of x and r is read: it may go over either.
-// Memory bounds it: 16384 x 4096 f16 91 us (5.9 TB/s), 124800 x 128 bf16 22 us, in 8 bits
-// 124800 x 64 bf16 14 us (4.0 TB/s; products in 32 bits instead of 64 changed nothing), one
-// row of 1024 3.1 us.
+// Memory bounds it: 16384 x 4096 f16 91 us (5.9 TB/s), f32 186 (5.8), 124800 x 128 bf16 21, f32 42,
+// in 8 bits 124800 x 64 bf16 13 us (4.2 TB/s; products in 32 bits instead of 64 changed nothing),
+// one row of 1024 2.9 us.
 //
 // N = 4: held to the 168 registers of three waves a SIMD (the 8-bit form of 16-bit rows would take a few
 // more: 4096 x 6000 f16 96 us for 92).
@@ -271,8 +271,10 @@ __global__ void __launch_bounds__(kNormThreads, N == 4 ? 3 : 1) k_rms_norm(NormA
 // dx = s g - u (s mean(g u)) + dh with g = dy w and the unit row u = h s, and this workgroup's
 // part of dw = sum over rows of dy u: each thread adds up its channels over its rows in
 // registers, the workgroup's groups are joined once at the end. Neither a power of s nor a
-// product with h is formed: those leave 32 bits (rows of 1e14, s^3 = 1e-42) where u does not. 16384 x 4096 f16 114 us
-// (4.7 TB/s) and 5 for the sum of the parts, 124800 x 128 bf16 22 us and 4.
+// product with h is formed: those leave 32 bits (rows of 1e14, s^3 = 1e-42) where u does not.
+// 16384 x 4096 f16 113 us (4.8 TB/s) and 5 for the sum of the parts, f32 212 (5.1) and 6, 124800 x 128
+// bf16 21 us and 5. N = 8 takes more than 256 registers, one wave a SIMD: 8192 x 8192 f32 211 us (5.1 TB/s)
+// all the same.
 template <typename T, int L, int N, bool kWeight>
 __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad(NormGradArgs a) {
   constexpr int V = Vec<T>::kN;
@@ -373,7 +375,9 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad(NormGradArgs a) 
 }
 
 // Rows of fewer channels than a vector has (L = 1: one thread a row), or of more
-// than a workgroup's registers hold (L = a workgroup, the row read twice).
+// than a workgroup's registers hold (L = a workgroup, the row read twice), element by
+// element: such rows are rare, and loads of 2 or 4 bytes a lane bound them. 2048 x 20000 bf16 142 us
+// for the 66 that its bytes take, in 8 bits 152 for 58, 2048 x 10000 f32 91 for 66, 124800 x 3 f32 5.
 template <typename T, int L, bool kI8>
 __global__ void __launch_bounds__(kNormThreads) k_rms_norm_any(NormArgs a) {
   __shared__ GroupScratch<float> s_red;
@@ -448,7 +452,8 @@ __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad_any(NormGradArgs
 }
 
 // The weight gradient's parts for the rows of k_rms_norm_grad_any: block (column
-// group, part) adds a contiguous range of rows.
+// group, part) adds a contiguous range of rows. Beside that kernel's 209 us for 2048 x 20000 bf16 it takes 68
+// and the sum of the parts 13; for 124800 x 3 f32, where three threads of a workgroup add, 18 beside 4.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) k_rms_norm_grad_part(NormGradArgs a, int parts, i64 rows_per_part) {
   const int groups = (a.channels + kNormThreads - 1) / kNormThreads;

@@ -36,10 +36,10 @@ __device__ __forceinline__ int w_key(int row) { return ((row >> 1) & 1) | ((row 
 // two steps between barriers, with the loads of the next two under way. Otherwise, from any
 // address, through registers: loaded two steps ahead, written one step ahead.
 //
-// 16384 x 4096 -> 4096: 233 us, 2360 TOP/s (a library's 8-bit product of this size: 1990): the
-// matrix units are busy 56% of the cycles at the 2.0 GHz the card holds under this load.
-// One barrier a step: 248 us; loads spread among the products instead of after the
-// barrier: 243; the second step's reads among the first's products: no change.
+// 16384 x 4096 -> 4096: 217 to 233 us from one card to another, 2360 to 2530 TOP/s (a library's 8-bit
+// product of this size: 1990): the matrix units are busy 54% of the cycles at the 2.2 GHz the card holds
+// under this load. Where this takes 233: one barrier a step 248 us; loads spread among the products instead
+// of after the barrier 243; the second step's reads among the first's products no change.
 // 124800 x 256 -> 768: 57 us, 224 MB at 3.9 TB/s: bound by the stores (33 us without them).
 template <typename T, int BM, int BN, int WM, int kBufs, int kPer, bool kDirect>
 __global__ void __launch_bounds__((BM / WM) * (BN / 64) * 64)
@@ -345,7 +345,17 @@ bool aligned_16(const void* p, i64 stride) { return (((uintptr_t)p | (uintptr_t)
 // A tile's loads and products grow as its area, its traffic as its edge: the largest tile that
 // fills the card is best, but 256 x 256 runs one workgroup a CU, whose stores nothing hides
 // when the input channels are few. Through registers (unaligned) the order is the same
-// ((a) with 4095 input channels: 296, 390, 842).
+// ((a) with 4095 input channels: 296, 390, 842). The 64x64 tile against the best of the splits
+// (4x2 but for two of them), around half as many tiles as CUs (128 here):
+//   tiles                            64x64   split
+//   128   1024 x 4096 -> 512          19.4    15.0
+//   128   1024 x 256 -> 512            5.2     5.0
+//   130   640 x 1024 -> 832            7.2     9.2
+//   144   1003 x 601 -> 523, f32       6.9    11.0
+//   144   1024 x 4096 -> 576          19.5    25.0
+//   192   768 x 4096 -> 1024          19.2    24.7
+//   256   1024 x 256 -> 1024           5.1     6.1
+// A split of 130 tiles' work needs a second round of workgroups.
 template <typename T>
 void plain_product(const ProductArgs& a, hipStream_t s) {
   const i64 cus = device_cu_count();
