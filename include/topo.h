@@ -432,6 +432,109 @@ tc_status tc_sparse_conv_i8(const int8_t* d_x, int64_t x_stride, const float* d_
                             const float* d_w_scale, const float* d_bias, int32_t c_out, int32_t c_in,
                             int32_t out_dtype, void* d_out, int64_t out_stride, void* stream);
 
+/* Layer norm of every row with the residual's addition (training form):
+ *   h = x + r, rounded to dtype; m = mean(h), s = 1 / sqrt(mean((h - m)^2) + eps);
+ *   out = (h - m) s w + b, rounded to dtype.
+ * The norm is that of the rounded h. m is a 64-bit sum, held as two floats, so that rows far from zero keep
+ * the digits of their spread; the squares' sum is a 32-bit float, or a 64-bit one where the squares near the
+ * ends of 32 bits, so every finite row has its norm.
+ *   d_x         dtype[n_rows][channels], x_stride.
+ *   d_residual  dtype[n_rows][channels], residual_stride, or NULL (h = x).
+ *   d_weight    weight_dtype[channels] (TC_F32, or dtype), or NULL (ones).
+ *   d_bias      bias_dtype[channels] (TC_F32, or dtype), or NULL (zeros).
+ *   eps         finite, >= 0.
+ *   d_sum       dtype[n_rows][channels]: h, or NULL. With contiguous rows it may
+ *               be d_x or d_residual itself.
+ *   d_out       dtype[n_rows][channels].
+ *   d_mean      float[n_rows]: m rounded to 32 bits, or NULL.
+ *   d_rstd      float[n_rows]: s (infinite where it leaves 32 bits), or NULL. */
+tc_status tc_layer_norm(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
+                        const void* d_weight, int32_t weight_dtype, const void* d_bias, int32_t bias_dtype,
+                        int64_t n_rows, int32_t channels, int32_t dtype, float eps, void* d_sum, void* d_out,
+                        float* d_mean, float* d_rstd, void* stream);
+
+/* Gradient of tc_layer_norm. With dy the gradient of out, dh that of h by its other
+ * uses (the residual stream), g = dy w and u = (h - m) s:
+ *   grad_x = s (g - mean(g) - u mean(g u)) + dh, rounded to dtype: the gradient of x, and of r alike;
+ *   grad_weight = sum over rows of dy u, grad_bias = sum over rows of dy: 32-bit float sums in an order
+ *   that only n_rows, channels and dtype decide.
+ * m is h's mean as the row has it; d_mean, its rounding to 32 bits, is where the sums start from.
+ *   d_grad_out    dtype[n_rows][channels], grad_out_stride.
+ *   d_grad_sum    dh, dtype[n_rows][channels], grad_sum_stride, or NULL (zeros).
+ *   d_h           h as tc_layer_norm left it (x where there is no residual), h_stride.
+ *   d_mean, d_rstd  float[n_rows] as tc_layer_norm left them.
+ *   d_grad_x      dtype[n_rows][channels], or NULL. With contiguous rows it may be
+ *                 d_grad_sum itself.
+ *   d_grad_weight, d_grad_bias  float[channels], or NULL (not all three NULL). Zeros without rows.
+ *   d_workspace   tc_layer_norm_backward_workspace(n_rows, channels) bytes, 16-byte
+ *                 aligned, read and written in stream order; may be NULL when
+ *                 d_grad_weight and d_grad_bias are. */
+tc_status tc_layer_norm_backward(const void* d_grad_out, int64_t grad_out_stride, const void* d_grad_sum,
+                                 int64_t grad_sum_stride, const void* d_h, int64_t h_stride, const void* d_weight,
+                                 int32_t weight_dtype, const float* d_mean, const float* d_rstd, int64_t n_rows,
+                                 int32_t channels, int32_t dtype, void* d_grad_x, float* d_grad_weight,
+                                 float* d_grad_bias, void* d_workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of d_workspace; 0 for arguments that tc_layer_norm_backward refuses. */
+int64_t tc_layer_norm_backward_workspace(int64_t n_rows, int32_t channels);
+
+/* Rotary positions: the pairs of every head of a row are turned by angles that the row's
+ * integer coordinates decide (a voxel's x, y, z as tc_enumerate_ijk gives them, or a token's time,
+ * height and width). Pair i of an axis a has the angle t = positions[row][a] * freqs[i] radians:
+ *   (x1, x2) -> (x1 cos t - x2 sin t, x1 sin t + x2 cos t), rounded to dtype;
+ * with `inverse` by -t, which is the gradient too. Any coordinate and finite frequency: angles are
+ * reduced in 64 bits, and cos and sin are off by at most 2^-23.
+ *   d_x          dtype[n_rows][heads][dim] with unit stride in a head, x_row_stride and
+ *                x_head_stride elements between rows and heads (at least 0). dim 2 to 4096, heads 1 to 2^20.
+ *   d_positions  int32[n_rows][n_axes], position_stride elements between rows (at least 0).
+ *   h_sections   host int32[n_axes], n_axes 1 to 4: how many pairs each axis turns, one axis's pairs after
+ *                another's (an axis may have none); together `pairs`, 1 to dim / 2.
+ *   d_freqs      float[pairs]: radians for a step along the pair's axis.
+ *   interleaved  1: pair i is channels 2 i and 2 i + 1; 0: channels i and pairs + i.
+ *                Channels from 2 * pairs on are copied.
+ *   d_out        dtype[n_rows][heads][dim] with its own strides; rows and heads may not overlap
+ *                one another. It may be d_x itself, with the same strides. */
+tc_status tc_rotary(const void* d_x, int64_t x_row_stride, int64_t x_head_stride, int64_t n_rows, int32_t heads,
+                    int32_t dim, int32_t dtype, const int32_t* d_positions, int64_t position_stride, int32_t n_axes,
+                    const int32_t* h_sections, const float* d_freqs, int32_t interleaved, int32_t inverse, void* d_out,
+                    int64_t out_row_stride, int64_t out_head_stride, void* stream);
+
+/* Rows in microscaled 4 bits: blocks of 32 channels under one power of two (the last
+ * block of a row may have fewer). A value is sign, two bits of exponent and one of
+ * mantissa: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives (codes 0 to 7, 8 to 15). Of a block with the largest
+ * magnitude a:
+ *   E = max(floor(log2 a) - 2, -127), or -127 for a = 0; q = x 2^-E rounded to nearest even, at most 6;
+ *   scale = E + 127, so that q 2^(scale - 127) stands for x.
+ * A block with an infinity or NaN has q = 0 and scale = 255, which stands for NaN.
+ *   d_x      dtype[n_rows][channels], x_stride.
+ *   d_q      uint8[n_rows][ceil(channels / 2)], contiguous: channel 2 i in the low four bits of byte i, 2 i + 1
+ *            in the high ones (0 beyond an odd number of channels).
+ *   d_scale  uint8[n_rows][ceil(channels / 32)], contiguous. */
+tc_status tc_quantise_mx4(const void* d_x, int64_t x_stride, int64_t n_rows, int32_t channels, int32_t dtype,
+                          uint8_t* d_q, uint8_t* d_scale, void* stream);
+
+/* The values that such rows stand for, rounded to out_dtype (NaN under a scale of 255; a value beyond out_dtype's
+ * range is infinite).
+ *   d_q      uint8[n_rows][ceil(channels / 2)], q_stride bytes; d_scale uint8[n_rows][ceil(channels / 32)],
+ *            scale_stride bytes.
+ *   d_out    out_dtype[n_rows][channels], contiguous. */
+tc_status tc_dequantise_mx4(const uint8_t* d_q, int64_t q_stride, const uint8_t* d_scale, int64_t scale_stride,
+                            int64_t n_rows, int32_t channels, int32_t out_dtype, void* d_out, void* stream);
+
+/* Product of such rows with such weights:
+ *   out[m][n] = sum over blocks of 2^(x_scale + w_scale - 254) sum_c x[m][c] w[n][c] + bias[n], rounded to out_dtype.
+ * Sums are 32-bit floats in an order that only the sizes, alignments and strides decide. A scale of 255 makes the outputs that its block
+ * goes into NaN. Sums beyond 32 bits are infinite, or NaN.
+ *   d_x      uint8[n_rows][ceil(c_in / 2)], x_stride bytes; d_x_scale uint8[n_rows][ceil(c_in / 32)],
+ *            x_scale_stride bytes. The high bits of the last byte of an odd c_in may hold anything.
+ *   d_w      uint8[c_out][ceil(c_in / 2)], w_stride; d_w_scale uint8[c_out][ceil(c_in / 32)], w_scale_stride.
+ *   d_bias   float[c_out], or NULL.
+ *   d_out    out_dtype[n_rows][c_out], out_stride >= c_out elements. */
+tc_status tc_matmul_mx4(const uint8_t* d_x, int64_t x_stride, const uint8_t* d_x_scale, int64_t x_scale_stride,
+                        const uint8_t* d_w, int64_t w_stride, const uint8_t* d_w_scale, int64_t w_scale_stride,
+                        const float* d_bias, int64_t n_rows, int32_t c_out, int32_t c_in, int32_t out_dtype,
+                        void* d_out, int64_t out_stride, void* stream);
+
 /* Cached device memory: every call takes its scratch arrays (and the buffers
  * of intermediate batches) from blocks cached process-wide per device, stream
  * and allocator, and keeps them for the next call with the same key (reuse is

@@ -33,7 +33,8 @@ ABI_SYMBOLS = [
     "tc_debug_inject_flags", "tc_build_kernel_map_noalloc", "tc_profile_enable", "tc_profile_read",
     "tc_profile_disable", "tc_build_batched_topology_many", "tc_enumerate_ijk_many", "tc_debug_wide_loads",
     "tc_rms_norm", "tc_rms_norm_i8", "tc_rms_norm_backward", "tc_rms_norm_backward_workspace", "tc_matmul_i8",
-    "tc_sparse_conv_i8",
+    "tc_sparse_conv_i8", "tc_layer_norm", "tc_layer_norm_backward", "tc_layer_norm_backward_workspace", "tc_rotary",
+    "tc_quantise_mx4", "tc_dequantise_mx4", "tc_matmul_mx4",
 ]
 
 HEADER_DTYPE = np.dtype([
@@ -167,6 +168,21 @@ def load_library(path: str = LIB_PATH):
         lib.tc_matmul_i8.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, i32, i32, i32, vp, i64, vp]
         lib.tc_sparse_conv_i8.restype = ctypes.c_int
         lib.tc_sparse_conv_i8.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, vp, vp, i32, i32, i32, vp, i64, vp]
+        lib.tc_layer_norm.restype = ctypes.c_int
+        lib.tc_layer_norm.argtypes = [vp, i64, vp, i64, vp, i32, vp, i32, i64, i32, i32, f32, vp, vp, vp, vp, vp]
+        lib.tc_layer_norm_backward.restype = ctypes.c_int
+        lib.tc_layer_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i32, vp, vp, i64, i32, i32, vp, vp, vp, vp,
+                                               i64, vp]
+        lib.tc_layer_norm_backward_workspace.restype = i64
+        lib.tc_layer_norm_backward_workspace.argtypes = [i64, i32]
+        lib.tc_rotary.restype = ctypes.c_int
+        lib.tc_rotary.argtypes = [vp, i64, i64, i64, i32, i32, i32, vp, i64, i32, vp, vp, i32, i32, vp, i64, i64, vp]
+        lib.tc_quantise_mx4.restype = ctypes.c_int
+        lib.tc_quantise_mx4.argtypes = [vp, i64, i64, i32, i32, vp, vp, vp]
+        lib.tc_dequantise_mx4.restype = ctypes.c_int
+        lib.tc_dequantise_mx4.argtypes = [vp, i64, vp, i64, i64, i32, i32, vp, vp]
+        lib.tc_matmul_mx4.restype = ctypes.c_int
+        lib.tc_matmul_mx4.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, i64, vp]
         if lib.tc_abi_version() != 1:
             raise ImportError("libtopo.so ABI version mismatch")
         _lib = lib
@@ -530,6 +546,8 @@ class _Ops:
         f.set_error(TopoError)
         self.rms_norm, self.rms_norm_i8, self.rms_norm_backward = f.rms_norm, f.rms_norm_i8, f.rms_norm_backward
         self.matmul_i8, self.sparse_conv_i8 = f.matmul_i8, f.sparse_conv_i8
+        self.layer_norm, self.layer_norm_backward, self.rotary = f.layer_norm, f.layer_norm_backward, f.rotary
+        self.quantise_mx4, self.dequantise_mx4, self.matmul_mx4 = f.quantise_mx4, f.dequantise_mx4, f.matmul_mx4
         self.on_stream = torch.cuda.stream
         # without a GPU no tensor passes the checks, whatever the device
         self.device = getattr(torch._C, "_cuda_getDevice") if torch.cuda.is_available() else lambda: -1
@@ -537,6 +555,8 @@ class _Ops:
         self.stream = raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)
         self.records = f.records
         self.norm_function = _norm_function(self)
+        self.layer_norm_function = _layer_norm_function(self)
+        self.rotary_function = _rotary_function(self)
 
     def call(self, f, stream, *args):
         """f on the current stream, or on `stream` and its device: outputs are taken on the stream they are written on."""
@@ -547,12 +567,15 @@ class _Ops:
             return f(*args, self.device(), stream.cuda_stream)
 
 
+def _unit_stride(grad):
+    """A gradient may come with any strides; the operators take unit stride in the last dimension."""
+    return grad if grad.stride(-1) == 1 or grad.shape[-1] == 1 else grad.contiguous()
+
+
 def _norm_function(ops):
     """tc_rms_norm as an autograd function; its backward is tc_rms_norm_backward."""
     import torch
-
-    def rows(grad):  # a gradient may come with any strides
-        return grad if grad.stride(1) == 1 or grad.shape[1] == 1 else grad.contiguous()
+    rows = _unit_stride
 
     class RmsNorm(torch.autograd.Function):
         """(out, rstd), and h between them where there is a residual: without one h is x itself,
@@ -581,6 +604,66 @@ def _norm_function(ops):
             return grad if needs[0] else None, grad_weight if needs[1] else None, grad if needs[2] else None, None
 
     return RmsNorm.apply
+
+
+def _layer_norm_function(ops):
+    """tc_layer_norm as an autograd function; its backward is tc_layer_norm_backward."""
+    import torch
+    rows = _unit_stride
+
+    class LayerNorm(torch.autograd.Function):
+        """(out, mean, rstd), and h after out where there is a residual, as for the root-mean-square norm."""
+
+        @staticmethod
+        def forward(ctx, x, weight, bias, residual, eps):
+            out, h, mean, rstd = ops.call(ops.layer_norm, None, x, weight, bias, residual, eps)
+            ctx.save_for_backward(h, weight, mean, rstd)
+            ctx.bias_dtype = None if bias is None else bias.dtype
+            ctx.set_materialize_grads(False)
+            ctx.mark_non_differentiable(mean, rstd)
+            return (out, mean, rstd) if residual is None else (out, h, mean, rstd)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, grad_out, *grad_rest):
+            h, weight, mean, rstd = ctx.saved_tensors
+            needs = ctx.needs_input_grad
+            grad_h = grad_rest[0] if len(grad_rest) == 3 else None
+            grad, grad_weight, grad_bias = grad_h, None, None
+            if grad_out is not None:
+                grad, grad_weight, grad_bias = ops.call(ops.layer_norm_backward, None, rows(grad_out), h, weight, mean,
+                                                        rstd, None if grad_h is None else rows(grad_h), needs[2])
+                if grad_weight is not None:
+                    grad_weight = grad_weight.to(weight.dtype)
+                if grad_bias is not None:
+                    grad_bias = grad_bias.to(ctx.bias_dtype)
+            return (grad if needs[0] else None, grad_weight if needs[1] else None, grad_bias, grad if needs[3] else None,
+                    None)
+
+    return LayerNorm.apply
+
+
+def _rotary_function(ops):
+    """tc_rotary as an autograd function: its backward is the inverse turn."""
+    import torch
+
+    class Rotary(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, positions, freqs, sections, interleaved, inverse):
+            ctx.save_for_backward(positions, freqs)
+            ctx.how = sections, interleaved, inverse
+            return ops.call(ops.rotary, None, x, positions, freqs, sections, interleaved, inverse, None)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, grad):
+            positions, freqs = ctx.saved_tensors
+            sections, interleaved, inverse = ctx.how
+            grad = ops.call(ops.rotary, None, _unit_stride(grad), positions, freqs, sections, interleaved, not inverse,
+                            None)
+            return grad, None, None, None, None, None
+
+    return Rotary.apply
 
 
 _ops_state = None
@@ -639,6 +722,73 @@ def tc_sparse_conv_i8(x, x_scale, kmap, w, w_scale, bias=None, out_dtype=None, o
     bias and output as for tc_matmul_i8."""
     ops = _ops()
     return ops.call(ops.sparse_conv_i8, stream, x, x_scale, kmap, w, w_scale, bias, out_dtype, out)
+
+
+def tc_layer_norm(x, weight=None, bias=None, residual=None, eps: float = 1e-5, stream=None):
+    """Layer norm of rows: h = x + residual, m = mean(h), s = 1 / sqrt(mean((h - m)^2) + eps),
+    out = (h - m) * s * weight + bias. Returns (out, h, mean, rstd): h is x itself without a residual, mean and rstd
+    float32 [rows] are m and s, kept for tc_layer_norm_backward. Where autograd records (x, weight, bias or
+    residual requires a gradient), out and h carry the graph; mean and rstd never do, and there are no second
+    derivatives and no forward-mode tangents."""
+    ops = _ops()
+    if ops.records(x, weight, bias, residual):
+        if stream is not None:  # the backward runs on the stream that the forward was recorded on
+            with ops.on_stream(stream):
+                return tc_layer_norm(x, weight, bias, residual, eps)
+        r = ops.layer_norm_function(x, weight, bias, residual, eps)
+        return r if residual is not None else (r[0], x, r[1], r[2])
+    return ops.call(ops.layer_norm, stream, x, weight, bias, residual, eps)
+
+
+def tc_layer_norm_backward(grad_out, h, weight, mean, rstd, grad_h=None, with_bias: bool = True, stream=None):
+    """Gradient of tc_layer_norm from what it returned: (grad_x, grad_weight, grad_bias). grad_x is
+    the gradient of x and of the residual alike, `grad_h` (if given) that of h by its other uses; grad_weight and
+    grad_bias are float32 [channels], None without a weight or `with_bias`."""
+    ops = _ops()
+    return ops.call(ops.layer_norm_backward, stream, grad_out, h, weight, mean, rstd, grad_h, with_bias)
+
+
+def tc_rotary(x, positions, freqs, sections=None, interleaved: bool = False, inverse: bool = False, out=None,
+              stream=None):
+    """Rotary positions: the pairs of every head of x [rows, heads, dim] (or [rows, dim]) are turned by
+    positions[row, axis] * freqs[pair] radians. positions int32 [rows, axes], 1 to 4 axes (a batch's tc_enumerate_ijk, or a
+    token's time, height and width); `sections` says how many pairs each axis turns, freqs float32 [pairs] by
+    how much a step. Pair i is channels i and pairs + i, or `interleaved` 2 i and 2 i + 1; channels from 2 * pairs on are
+    copied. `inverse` turns back. The result is a new tensor, or goes into `out` (which may be x). Where autograd
+    records, x may require a gradient (`out` is refused then), positions and freqs may not."""
+    ops = _ops()
+    if ops.records(freqs):
+        raise ValueError("freqs requires a gradient, which this call has none for")
+    if ops.records(x):
+        if out is not None:
+            raise ValueError("out cannot be given where a gradient is recorded")
+        if stream is not None:  # as tc_rms_norm
+            with ops.on_stream(stream):
+                return tc_rotary(x, positions, freqs, sections, interleaved, inverse)
+        return ops.rotary_function(x, positions, freqs, sections, interleaved, inverse)
+    return ops.call(ops.rotary, stream, x, positions, freqs, sections, interleaved, inverse, out)
+
+
+def tc_quantise_mx4(x, stream=None):
+    """Rows in microscaled 4 bits: (q uint8 [rows, ceil(channels / 2)], two channels a byte, the even one in its low
+    half; scale uint8 [rows, ceil(channels / 32)], the exponent of each block of 32 plus 127). Nothing is
+    recorded for a gradient."""
+    ops = _ops()
+    return ops.call(ops.quantise_mx4, stream, x)
+
+
+def tc_dequantise_mx4(q, scale, channels=None, out_dtype=None, stream=None):
+    """The values that 4-bit rows stand for: [rows, channels] of `out_dtype` (bfloat16 unless given). `channels` is needed
+    where it is odd."""
+    ops = _ops()
+    return ops.call(ops.dequantise_mx4, stream, q, scale, channels, out_dtype)
+
+
+def tc_matmul_mx4(x, x_scale, w, w_scale, channels=None, bias=None, out_dtype=None, out=None, stream=None):
+    """Product of 4-bit rows (x, x_scale) with 4-bit weights (w, w_scale), both as tc_quantise_mx4 lays them out, [rows, c_in]
+    and [c_out, c_in]; `channels` is c_in, needed where it is odd. float32 bias [c_out]; output as for tc_matmul_i8."""
+    ops = _ops()
+    return ops.call(ops.matmul_mx4, stream, x, x_scale, w, w_scale, channels, bias, out_dtype, out)
 
 
 def tc_scratch_release():

@@ -22,7 +22,7 @@ ARCH = os.environ.get("TOPO_OFFLOAD_ARCH", "gfx950")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["runtime.hip", "primitives.hip", "tree.hip", "pass.hip", "from_ijk.hip", "points.hip", "kmap.hip",
-           "norm.hip", "product.hip", "conv.hip", "abi.hip"]
+           "norm.hip", "product.hip", "conv.hip", "layer_norm.hip", "rotary.hip", "mx4.hip", "product_mx4.hip", "abi.hip"]
 
 COMMON = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

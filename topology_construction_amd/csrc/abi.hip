@@ -328,6 +328,14 @@ void check_rows(const void* p, int64_t stride, int64_t n_rows, const char* name)
   if (stride < 0) throw tc::Error(TC_ERR_INVALID_ARG, std::string(name) + ": negative row stride");
 }
 
+// Whether `n` runs of `each` elements, `step` apart, do not overlap, nor `outer` groups of them, `outer_step` apart.
+bool nested(int64_t each, int64_t n, int64_t step, int64_t outer, int64_t outer_step) {
+  if (n > 1 && step < each) return false;
+  if (outer == 1) return true;
+  if (n > 1 && step > (INT64_MAX - each) / (n - 1)) return false;
+  return outer_step >= (n > 1 ? step * (n - 1) : 0) + each;
+}
+
 tc::NormArgs norm_args(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
                        const void* d_weight, int32_t weight_dtype, int64_t n_rows, int32_t channels, int32_t dtype,
                        float eps, void* d_sum) {
@@ -934,6 +942,218 @@ tc_status tc_sparse_conv_i8(const int8_t* d_x, int64_t x_stride, const float* d_
     a.out_stride = out_stride;
     check_product(a);
     tc::product_i8(a, (hipStream_t)stream);
+    return TC_OK;
+  });
+}
+
+tc_status tc_layer_norm(const void* d_x, int64_t x_stride, const void* d_residual, int64_t residual_stride,
+                        const void* d_weight, int32_t weight_dtype, const void* d_bias, int32_t bias_dtype,
+                        int64_t n_rows, int32_t channels, int32_t dtype, float eps, void* d_sum, void* d_out,
+                        float* d_mean, float* d_rstd, void* stream) {
+  return guarded([&]() {
+    check_norm_shape(n_rows, channels, dtype, d_weight, weight_dtype);
+    need(!d_bias || bias_dtype == TC_F32 || bias_dtype == dtype, "bias_dtype must be TC_F32 or dtype");
+    check_rows(d_x, x_stride, n_rows, "d_x");
+    if (d_residual) check_rows(d_residual, residual_stride, n_rows, "d_residual");
+    need(std::isfinite(eps) && eps >= 0.0f, "eps must be finite and not negative");
+    need(d_out || n_rows == 0, "d_out is NULL");
+    tc::LayerNormArgs a{};
+    a.x = d_x;
+    a.x_stride = x_stride;
+    a.residual = d_residual;
+    a.residual_stride = residual_stride;
+    a.weight = d_weight;
+    a.weight_dtype = weight_dtype;
+    a.bias = d_bias;
+    a.bias_dtype = bias_dtype;
+    a.rows = n_rows;
+    a.channels = channels;
+    a.dtype = dtype;
+    a.eps = eps;
+    a.sum = d_sum;
+    a.out = d_out;
+    a.mean = d_mean;
+    a.rstd = d_rstd;
+    tc::layer_norm(a, (hipStream_t)stream);
+    return TC_OK;
+  });
+}
+
+tc_status tc_layer_norm_backward(const void* d_grad_out, int64_t grad_out_stride, const void* d_grad_sum,
+                                 int64_t grad_sum_stride, const void* d_h, int64_t h_stride, const void* d_weight,
+                                 int32_t weight_dtype, const float* d_mean, const float* d_rstd, int64_t n_rows,
+                                 int32_t channels, int32_t dtype, void* d_grad_x, float* d_grad_weight,
+                                 float* d_grad_bias, void* d_workspace, int64_t workspace_bytes, void* stream) {
+  return guarded([&]() {
+    check_norm_shape(n_rows, channels, dtype, d_weight, weight_dtype);
+    check_rows(d_grad_out, grad_out_stride, n_rows, "d_grad_out");
+    if (d_grad_sum) check_rows(d_grad_sum, grad_sum_stride, n_rows, "d_grad_sum");
+    check_rows(d_h, h_stride, n_rows, "d_h");
+    need((d_mean && d_rstd) || n_rows == 0, "d_mean or d_rstd is NULL");
+    need(d_grad_x || d_grad_weight || d_grad_bias || n_rows == 0, "d_grad_x, d_grad_weight and d_grad_bias are all NULL");
+    if (d_grad_weight || d_grad_bias) {
+      need(d_workspace != nullptr, "d_workspace is NULL");
+      need(workspace_bytes >= 0 && (size_t)workspace_bytes >= tc::layer_norm_grad_workspace(n_rows, channels),
+           "workspace_bytes below tc_layer_norm_backward_workspace");
+      need(((uintptr_t)d_workspace & 15) == 0, "d_workspace is not 16-byte aligned");
+    }
+    tc::LayerNormGradArgs a{};
+    a.grad_out = d_grad_out;
+    a.grad_out_stride = grad_out_stride;
+    a.grad_sum = d_grad_sum;
+    a.grad_sum_stride = grad_sum_stride;
+    a.h = d_h;
+    a.h_stride = h_stride;
+    a.weight = d_weight;
+    a.weight_dtype = weight_dtype;
+    a.mean = d_mean;
+    a.rstd = d_rstd;
+    a.rows = n_rows;
+    a.channels = channels;
+    a.dtype = dtype;
+    a.grad_x = d_grad_x;
+    a.grad_weight = d_grad_weight;
+    a.grad_bias = d_grad_bias;
+    a.partial = static_cast<float*>(d_workspace);
+    tc::layer_norm_grad(a, (hipStream_t)stream);
+    return TC_OK;
+  });
+}
+
+int64_t tc_layer_norm_backward_workspace(int64_t n_rows, int32_t channels) {
+  if (n_rows < 0 || channels < 1 || channels > kMaxChannels) return 0;
+  return (int64_t)tc::layer_norm_grad_workspace(n_rows, channels);
+}
+
+tc_status tc_rotary(const void* d_x, int64_t x_row_stride, int64_t x_head_stride, int64_t n_rows, int32_t heads,
+                    int32_t dim, int32_t dtype, const int32_t* d_positions, int64_t position_stride, int32_t n_axes,
+                    const int32_t* h_sections, const float* d_freqs, int32_t interleaved, int32_t inverse, void* d_out,
+                    int64_t out_row_stride, int64_t out_head_stride, void* stream) {
+  return guarded([&]() {
+    need(n_rows >= 0, "n_rows is negative");
+    need(heads >= 1 && dim >= 2, "heads must be positive and dim at least 2");
+    need(is_dtype(dtype), "unknown dtype");
+    if (dim > 4096) throw tc::Error(TC_ERR_UNSUPPORTED, "dim above 4096");
+    if (heads > kMaxChannels) throw tc::Error(TC_ERR_UNSUPPORTED, "more than 2^20 heads");
+    need(n_axes >= 1 && n_axes <= 4, "n_axes must be in [1, 4]");
+    need(h_sections != nullptr, "h_sections is NULL");
+    tc::RotaryArgs a{};
+    int64_t pairs = 0;
+    for (int i = 0; i < n_axes; ++i) {
+      need(h_sections[i] >= 0, "a section is negative");
+      pairs += h_sections[i];
+      if (i < 3) a.ends[i] = i + 1 < n_axes ? (int)std::min<int64_t>(pairs, INT32_MAX) : INT32_MAX;
+    }
+    for (int i = n_axes; i < 3; ++i) a.ends[i] = INT32_MAX;
+    need(pairs >= 1 && 2 * pairs <= dim, "the sections must add up to 1 to dim / 2 pairs");
+    need(interleaved == 0 || interleaved == 1, "interleaved must be 0 or 1");
+    need(inverse == 0 || inverse == 1, "inverse must be 0 or 1");
+    check_rows(d_x, x_row_stride, n_rows, "d_x");
+    need(x_head_stride >= 0, "d_x: negative head stride");
+    check_rows(d_positions, position_stride, n_rows, "d_positions");
+    need(d_freqs || n_rows == 0, "d_freqs is NULL");
+    need(d_out || n_rows == 0, "d_out is NULL");
+    need(out_row_stride >= 0 && out_head_stride >= 0, "d_out: negative stride");
+    if (n_rows > 0) {
+      // heads inside rows, or rows inside heads
+      need(nested(dim, heads, out_head_stride, n_rows, out_row_stride) ||
+               nested(dim, n_rows, out_row_stride, heads, out_head_stride),
+           "the rows or heads of d_out overlap");
+    }
+    a.x = d_x;
+    a.x_row = x_row_stride;
+    a.x_head = x_head_stride;
+    a.rows = n_rows;
+    a.heads = heads;
+    a.dim = dim;
+    a.pairs = (int)pairs;
+    a.dtype = dtype;
+    a.positions = d_positions;
+    a.position_row = position_stride;
+    a.freqs = d_freqs;
+    a.interleaved = interleaved == 1;
+    a.inverse = inverse == 1;
+    a.out = d_out;
+    a.out_row = out_row_stride;
+    a.out_head = out_head_stride;
+    a.in_place = d_out == d_x && out_row_stride == x_row_stride && out_head_stride == x_head_stride;
+    tc::rotary(a, (hipStream_t)stream);
+    return TC_OK;
+  });
+}
+
+tc_status tc_quantise_mx4(const void* d_x, int64_t x_stride, int64_t n_rows, int32_t channels, int32_t dtype,
+                          uint8_t* d_q, uint8_t* d_scale, void* stream) {
+  return guarded([&]() {
+    check_norm_shape(n_rows, channels, dtype, nullptr, dtype);
+    check_rows(d_x, x_stride, n_rows, "d_x");
+    need((d_q && d_scale) || n_rows == 0, "d_q or d_scale is NULL");
+    tc::QuantiseArgs a{};
+    a.x = d_x;
+    a.x_stride = x_stride;
+    a.rows = n_rows;
+    a.channels = channels;
+    a.dtype = dtype;
+    a.q = d_q;
+    a.scale = d_scale;
+    tc::quantise_mx4(a, (hipStream_t)stream);
+    return TC_OK;
+  });
+}
+
+tc_status tc_dequantise_mx4(const uint8_t* d_q, int64_t q_stride, const uint8_t* d_scale, int64_t scale_stride,
+                            int64_t n_rows, int32_t channels, int32_t out_dtype, void* d_out, void* stream) {
+  return guarded([&]() {
+    check_norm_shape(n_rows, channels, out_dtype, nullptr, out_dtype);
+    check_rows(d_q, q_stride, n_rows, "d_q");
+    check_rows(d_scale, scale_stride, n_rows, "d_scale");
+    need(d_out || n_rows == 0, "d_out is NULL");
+    tc::DequantiseArgs a{};
+    a.q = d_q;
+    a.q_stride = q_stride;
+    a.scale = d_scale;
+    a.scale_stride = scale_stride;
+    a.rows = n_rows;
+    a.channels = channels;
+    a.out_dtype = out_dtype;
+    a.out = d_out;
+    tc::dequantise_mx4(a, (hipStream_t)stream);
+    return TC_OK;
+  });
+}
+
+tc_status tc_matmul_mx4(const uint8_t* d_x, int64_t x_stride, const uint8_t* d_x_scale, int64_t x_scale_stride,
+                        const uint8_t* d_w, int64_t w_stride, const uint8_t* d_w_scale, int64_t w_scale_stride,
+                        const float* d_bias, int64_t n_rows, int32_t c_out, int32_t c_in, int32_t out_dtype,
+                        void* d_out, int64_t out_stride, void* stream) {
+  return guarded([&]() {
+    need(n_rows >= 0, "n_rows is negative");
+    need(c_out >= 1 && c_in >= 1, "c_out and c_in must be positive");
+    need(is_dtype(out_dtype), "unknown out_dtype");
+    if (c_in > kMaxChannels || c_out > kMaxChannels) throw tc::Error(TC_ERR_UNSUPPORTED, "more than 2^20 channels");
+    check_rows(d_x, x_stride, n_rows, "d_x");
+    check_rows(d_x_scale, x_scale_stride, n_rows, "d_x_scale");
+    check_rows(d_w, w_stride, n_rows, "d_w");
+    check_rows(d_w_scale, w_scale_stride, n_rows, "d_w_scale");
+    need(d_out || n_rows == 0, "d_out is NULL");
+    need(out_stride >= c_out, "out_stride below c_out");
+    tc::ProductMx4Args a{};
+    a.x = d_x;
+    a.x_stride = x_stride;
+    a.x_scale = d_x_scale;
+    a.x_scale_stride = x_scale_stride;
+    a.w = d_w;
+    a.w_stride = w_stride;
+    a.w_scale = d_w_scale;
+    a.w_scale_stride = w_scale_stride;
+    a.bias = d_bias;
+    a.rows = n_rows;
+    a.n = c_out;
+    a.k = c_in;
+    a.out_dtype = out_dtype;
+    a.out = d_out;
+    a.out_stride = out_stride;
+    tc::product_mx4(a, (hipStream_t)stream);
     return TC_OK;
   });
 }

@@ -213,6 +213,202 @@ PyObject* rms_norm_backward(const Args& g) {
   return tuple<2>({grad_x, grad_weight});
 }
 
+// The caller's own tensor as a result: autograd sees that it was written.
+PyObject* written(PyObject* out) {
+  const Tensor& t = THPVariable_Unpack(out);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  return Py_NewRef(out);
+}
+
+// A vector of one number a channel, in 32 bits or the rows' own type; none: nullptr.
+struct Params {
+  void* p = nullptr;
+  int dt;
+};
+Params params(PyObject* o, const char* name, at::ScalarType rows_type, int device, int64_t n) {
+  Params r{nullptr, dtype_id(rows_type)};
+  if (o == Py_None) return r;
+  const Tensor& t = tensor(o, name);
+  r.dt = dtype_id(t.scalar_type());
+  r.p = vector(t, name, t.scalar_type(), device, n);
+  return r;
+}
+
+// (x, weight, bias, residual, eps) -> (out, h, mean, rstd)
+PyObject* layer_norm(const Args& g) {
+  const Tensor& x = tensor(g.a[0], "x");
+  const auto type = x.scalar_type();
+  const int dt = dtype_id(type), device = device_of(x, g.current);
+  const Matrix xm = matrix(x, "x", type, device);
+  const bool residual = g.a[3] != Py_None;
+  Matrix rm;
+  if (residual) rm = matrix(tensor(g.a[3], "residual"), "residual", type, device, xm.rows, xm.cols);
+  const Params w = params(g.a[1], "weight", type, device, xm.cols), b = params(g.a[2], "bias", type, device, xm.cols);
+  const int32_t channels = channels_of(xm.cols, "x");
+  const double eps = PyFloat_AsDouble(g.a[4]);
+  if (eps == -1.0 && PyErr_Occurred()) return nullptr;
+  Tensor out = empty(x, {xm.rows, xm.cols}, type), mean = empty(x, {xm.rows}, at::kFloat),
+         rstd = empty(x, {xm.rows}, at::kFloat);
+  Tensor h = residual ? empty(x, {xm.rows, xm.cols}, type) : x;
+  void *ph = residual ? h.data_ptr() : nullptr, *po = out.data_ptr();
+  float *pm = static_cast<float*>(mean.data_ptr()), *ps = static_cast<float*>(rstd.data_ptr());
+  unlocked([&]() {
+    return tc_layer_norm(xm.p, xm.stride, rm.p, rm.stride, w.p, w.dt, b.p, b.dt, xm.rows, channels, dt, (float)eps, ph,
+                         po, pm, ps, g.stream);
+  });
+  if (residual) return tuple<4>({out, h, mean, rstd});
+  PyObject* r = tuple<4>({out, std::nullopt, mean, rstd});
+  if (r) {  // h is the caller's own tensor
+    Py_DECREF(PyTuple_GET_ITEM(r, 1));
+    PyTuple_SET_ITEM(r, 1, Py_NewRef(g.a[0]));
+  }
+  return r;
+}
+
+// (grad_out, h, weight, mean, rstd, grad_h, with_bias) -> (grad_x, grad_weight, grad_bias)
+PyObject* layer_norm_backward(const Args& g) {
+  const Tensor& h = tensor(g.a[1], "h");
+  const auto type = h.scalar_type();
+  const int dt = dtype_id(type), device = device_of(h, g.current);
+  const Matrix hm = matrix(h, "h", type, device);
+  const Matrix gm = matrix(tensor(g.a[0], "grad_out"), "grad_out", type, device, hm.rows, hm.cols);
+  Matrix dm;
+  if (g.a[5] != Py_None) dm = matrix(tensor(g.a[5], "grad_h"), "grad_h", type, device, hm.rows, hm.cols);
+  const float* mean = static_cast<float*>(vector(tensor(g.a[3], "mean"), "mean", at::kFloat, device, hm.rows));
+  const float* rstd = static_cast<float*>(vector(tensor(g.a[4], "rstd"), "rstd", at::kFloat, device, hm.rows));
+  const Params w = params(g.a[2], "weight", type, device, hm.cols);
+  const int32_t channels = channels_of(hm.cols, "h");
+  const int with_bias = PyObject_IsTrue(g.a[6]);
+  if (with_bias < 0) return nullptr;
+  std::optional<Tensor> grad_weight, grad_bias;
+  Tensor work;
+  int64_t bytes = 0;
+  if (g.a[2] != Py_None) grad_weight = empty(h, {hm.cols}, at::kFloat);
+  if (with_bias) grad_bias = empty(h, {hm.cols}, at::kFloat);
+  if (grad_weight || grad_bias) {
+    bytes = tc_layer_norm_backward_workspace(hm.rows, channels);
+    work = empty(h, {std::max<int64_t>(bytes, 1)}, at::kByte);
+  }
+  Tensor grad_x = empty(h, {hm.rows, hm.cols}, type);
+  void *px = grad_x.data_ptr(), *pwork = bytes ? work.data_ptr() : nullptr;
+  float* pw = grad_weight ? static_cast<float*>(grad_weight->data_ptr()) : nullptr;
+  float* pb = grad_bias ? static_cast<float*>(grad_bias->data_ptr()) : nullptr;
+  unlocked([&]() {
+    return tc_layer_norm_backward(gm.p, gm.stride, dm.p, dm.stride, hm.p, hm.stride, w.p, w.dt, mean, rstd, hm.rows,
+                                  channels, dt, px, pw, pb, pwork, bytes, g.stream);
+  });
+  return tuple<3>({grad_x, grad_weight, grad_bias});
+}
+
+struct Heads {
+  void* p;
+  int64_t row, head, rows;
+  int32_t heads, dim;
+};
+// [rows, heads, dim], or [rows, dim] (one head), with unit stride in a head.
+Heads heads_of(const Tensor& t, const char* name, at::ScalarType type, int device) {
+  check_kind(t, name, type, device);
+  if (t.dim() != 2 && t.dim() != 3) bad_value(std::string(name) + " must be [rows, heads, dim] or [rows, dim]");
+  const int64_t last = t.dim() - 1, heads = t.dim() == 3 ? t.size(1) : 1;
+  if (t.stride(last) != 1 && t.size(last) > 1 && t.numel() > 0)
+    bad_value(std::string(name) + " must have unit stride in a head");
+  if (heads > INT32_MAX || t.size(last) > INT32_MAX) bad_value(std::string(name) + " has too many channels");
+  return {t.data_ptr(), t.stride(0), t.dim() == 3 ? t.stride(1) : 0, t.size(0), (int32_t)heads, (int32_t)t.size(last)};
+}
+
+// (x, positions, freqs, sections, interleaved, inverse, out) -> out
+PyObject* rotary(const Args& g) {
+  const Tensor &x = tensor(g.a[0], "x"), &positions = tensor(g.a[1], "positions"), &freqs = tensor(g.a[2], "freqs");
+  const auto type = x.scalar_type();
+  const int dt = dtype_id(type), device = device_of(x, g.current);
+  const Heads h = heads_of(x, "x", type, device);
+  const Matrix pm = matrix(positions, "positions", at::kInt, device, h.rows);
+  int32_t sections[4];
+  int64_t axes = pm.cols, pairs = 0;
+  if (axes < 1 || axes > 4) bad_value("positions must have 1 to 4 axes");
+  if (g.a[3] == Py_None) {
+    if (axes != 1) bad_value("sections are needed where positions have more than one axis");
+    pairs = freqs.numel();
+    if (pairs > INT32_MAX) bad_value("too many frequencies");
+    sections[0] = (int32_t)pairs;
+  } else {
+    PyObject* list = PySequence_Fast(g.a[3], "sections must be a sequence of integers");
+    if (!list) return nullptr;
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(list);
+    bool ok = n == axes;
+    for (Py_ssize_t i = 0; ok && i < n; ++i) {
+      int over = 0;
+      const long v = PyLong_AsLongAndOverflow(PySequence_Fast_GET_ITEM(list, i), &over);
+      if (v == -1 && PyErr_Occurred()) {
+        Py_DECREF(list);
+        return nullptr;
+      }
+      ok = !over && v >= 0 && v <= INT32_MAX;
+      sections[i] = (int32_t)v;
+      pairs += v;
+    }
+    Py_DECREF(list);
+    if (!ok) bad_value("sections must be a number of pairs for each axis of positions");
+  }
+  const float* pf = static_cast<float*>(vector(freqs, "freqs", at::kFloat, device, pairs));
+  const int interleaved = PyObject_IsTrue(g.a[4]), inverse = PyObject_IsTrue(g.a[5]);
+  if (interleaved < 0 || inverse < 0) return nullptr;
+  std::optional<Tensor> made;
+  Heads o;
+  if (g.a[6] == Py_None) {
+    made = empty(x, x.sizes(), type);
+    o = {made->data_ptr(), (int64_t)h.heads * h.dim, h.dim, h.rows, h.heads, h.dim};
+  } else {
+    const Tensor& out = tensor(g.a[6], "out");
+    if (c10::GradMode::is_enabled() && out.requires_grad())
+      bad_value("out requires a gradient, which this call has none for");
+    if (out.sizes() != x.sizes()) bad_value("out has another shape than x");
+    o = heads_of(out, "out", type, device);
+  }
+  if (h.heads > 0)
+    unlocked([&]() {
+      return tc_rotary(h.p, h.row, h.head, h.rows, h.heads, h.dim, dt, static_cast<int32_t*>(pm.p), pm.stride,
+                       (int32_t)axes, sections, pf, interleaved, inverse, o.p, o.row, o.head, g.stream);
+    });
+  return made ? THPVariable_Wrap(*made) : written(g.a[6]);
+}
+
+// (x) -> (q, scale)
+PyObject* quantise_mx4(const Args& g) {
+  const Tensor& x = tensor(g.a[0], "x");
+  const auto type = x.scalar_type();
+  const int dt = dtype_id(type);
+  const Matrix xm = matrix(x, "x", type, device_of(x, g.current));
+  const int32_t channels = channels_of(xm.cols, "x");
+  Tensor q = empty(x, {xm.rows, (xm.cols + 1) / 2}, at::kByte), scale = empty(x, {xm.rows, (xm.cols + 31) / 32}, at::kByte);
+  uint8_t *pq = static_cast<uint8_t*>(q.data_ptr()), *ps = static_cast<uint8_t*>(scale.data_ptr());
+  unlocked([&]() { return tc_quantise_mx4(xm.p, xm.stride, xm.rows, channels, dt, pq, ps, g.stream); });
+  return tuple<2>({q, scale});
+}
+
+struct Mx4 {
+  Matrix q, scale;
+};
+Mx4 mx4(PyObject* q, PyObject* scale, const char* name, int device, int64_t channels) {
+  const std::string s = std::string(name) + "_scale";
+  return {matrix(tensor(q, name), name, at::kByte, device, -1, (channels + 1) / 2),
+          matrix(tensor(scale, s.c_str()), s.c_str(), at::kByte, device, tensor(q, name).size(0), (channels + 31) / 32)};
+}
+// The channels of rows packed two a byte: as given, or all that the bytes hold. False with a Python error.
+bool channels_of_mx4(PyObject* given, const Tensor& q, const char* name, int64_t& channels) {
+  if (q.dim() != 2) bad_value(std::string(name) + " must be a [rows, bytes] tensor");
+  channels = 2 * q.size(1);
+  if (given != Py_None) {
+    const int64_t bytes = q.size(1);
+    channels = PyLong_AsLongLong(given);
+    if (channels == -1 && PyErr_Occurred()) return false;
+    if (channels < 0 || channels > 2 * bytes || channels < 2 * bytes - 1)
+      bad_value(std::string(name) + " holds " + std::to_string(2 * bytes) + " channels, or one less");
+  }
+  channels_of(channels, name);
+  return true;
+}
+
 struct ProductIn {
   const Tensor* x;
   Matrix xm;
@@ -237,7 +433,7 @@ struct ProductOut {
   Matrix m;
   int dt;
 };
-ProductOut product_out(const ProductIn& p, PyObject* out, PyObject* out_dtype, int64_t rows, int64_t cols) {
+ProductOut product_out(const Tensor& like, int device, PyObject* out, PyObject* out_dtype, int64_t rows, int64_t cols) {
   ProductOut o;
   auto type = at::kBFloat16;
   if (out_dtype != Py_None) {
@@ -246,7 +442,7 @@ ProductOut product_out(const ProductIn& p, PyObject* out, PyObject* out_dtype, i
   }
   if (out == Py_None) {
     o.dt = dtype_id(type);
-    o.made = empty(*p.x, {rows, cols}, type);
+    o.made = empty(like, {rows, cols}, type);
     o.m = {o.made->data_ptr(), cols, rows, cols};
     return o;
   }
@@ -254,17 +450,13 @@ ProductOut product_out(const ProductIn& p, PyObject* out, PyObject* out_dtype, i
   if (c10::GradMode::is_enabled() && t.requires_grad()) bad_value("out requires a gradient, which this call has none for");
   if (out_dtype != Py_None && type != t.scalar_type()) bad_value("out is of another type than out_dtype");
   o.dt = dtype_id(t.scalar_type());
-  o.m = matrix(t, "out", t.scalar_type(), p.device, rows, cols);
+  o.m = matrix(t, "out", t.scalar_type(), device, rows, cols);
   if (o.m.stride < cols && rows > 1) bad_value("the rows of out overlap");
   o.m.stride = std::max(o.m.stride, cols);
   return o;
 }
 PyObject* result(const ProductOut& o, PyObject* out) {
-  if (o.made) return THPVariable_Wrap(*o.made);
-  // autograd sees that the caller's tensor was written
-  const Tensor& t = THPVariable_Unpack(out);
-  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
-  return Py_NewRef(out);
+  return o.made ? THPVariable_Wrap(*o.made) : written(out);
 }
 
 // (x, x_scale, w, w_scale, bias, out_dtype, out) -> out
@@ -273,7 +465,7 @@ PyObject* matmul_i8(const Args& g) {
   if (w.dim() != 2) bad_value("w must be a [c_out, c_in] tensor");
   const ProductIn p = product_in(g.a[0], g.a[1], g.a[3], g.a[4], w.size(0), g.current);
   const Matrix wm = matrix(w, "w", at::kChar, p.device, -1, p.xm.cols);
-  const ProductOut o = product_out(p, g.a[6], g.a[5], p.xm.rows, wm.rows);
+  const ProductOut o = product_out(*p.x, p.device, g.a[6], g.a[5], p.xm.rows, wm.rows);
   unlocked([&]() {
     return tc_matmul_i8(static_cast<int8_t*>(p.xm.p), p.xm.stride, p.xs, static_cast<int8_t*>(wm.p), wm.stride, p.ws,
                         p.bias, p.xm.rows, (int32_t)wm.rows, (int32_t)p.xm.cols, o.dt, o.m.p, o.m.stride, g.stream);
@@ -293,12 +485,50 @@ PyObject* sparse_conv_i8(const Args& g) {
   if (w.size(0) != taps || w.size(2) != p.xm.cols || !w.is_contiguous())
     bad_value("w must be a contiguous [" + std::to_string(taps) + ", c_out, " + std::to_string(p.xm.cols) + "] tensor");
   if (taps > INT32_MAX) bad_value("kmap has too many taps");
-  const ProductOut o = product_out(p, g.a[7], g.a[6], n_dst, w.size(1));
+  const ProductOut o = product_out(*p.x, p.device, g.a[7], g.a[6], n_dst, w.size(1));
   const int32_t* pm = static_cast<int32_t*>(kmap.data_ptr());
   const int8_t* pw = static_cast<int8_t*>(w.data_ptr());
   unlocked([&]() {
     return tc_sparse_conv_i8(static_cast<int8_t*>(p.xm.p), p.xm.stride, p.xs, p.xm.rows, pm, n_dst, (int32_t)taps, pw,
                              p.ws, p.bias, (int32_t)w.size(1), (int32_t)p.xm.cols, o.dt, o.m.p, o.m.stride, g.stream);
+  });
+  return result(o, g.a[7]);
+}
+
+// (q, scale, channels, out_dtype) -> out
+PyObject* dequantise_mx4(const Args& g) {
+  const Tensor& q = tensor(g.a[0], "q");
+  int64_t channels;
+  if (!channels_of_mx4(g.a[2], q, "q", channels)) return nullptr;
+  const int device = device_of(q, g.current);
+  const Mx4 m = mx4(g.a[0], g.a[1], "q", device, channels);
+  const ProductOut o = product_out(q, device, Py_None, g.a[3], m.q.rows, channels);
+  unlocked([&]() {
+    return tc_dequantise_mx4(static_cast<uint8_t*>(m.q.p), m.q.stride, static_cast<uint8_t*>(m.scale.p), m.scale.stride,
+                             m.q.rows, (int32_t)channels, o.dt, o.m.p, g.stream);
+  });
+  return THPVariable_Wrap(*o.made);
+}
+
+// (x, x_scale, w, w_scale, channels, bias, out_dtype, out) -> out
+PyObject* matmul_mx4(const Args& g) {
+  const Tensor &x = tensor(g.a[0], "x"), &wt = tensor(g.a[2], "w");
+  int64_t channels;
+  if (!channels_of_mx4(g.a[4], x, "x", channels)) return nullptr;
+  const int device = device_of(x, g.current);
+  const Mx4 xm = mx4(g.a[0], g.a[1], "x", device, channels);
+  if (wt.dim() != 2) bad_value("w must be a [c_out, bytes] tensor");
+  const Mx4 wm = mx4(g.a[2], g.a[3], "w", device, channels);
+  const int64_t c_out = wt.size(0);
+  channels_of(c_out, "w");
+  const float* bias =
+      g.a[5] == Py_None ? nullptr : static_cast<float*>(vector(tensor(g.a[5], "bias"), "bias", at::kFloat, device, c_out));
+  const ProductOut o = product_out(x, device, g.a[7], g.a[6], xm.q.rows, c_out);
+  auto bytes = [](const Matrix& m) { return static_cast<uint8_t*>(m.p); };
+  unlocked([&]() {
+    return tc_matmul_mx4(bytes(xm.q), xm.q.stride, bytes(xm.scale), xm.scale.stride, bytes(wm.q), wm.q.stride,
+                         bytes(wm.scale), wm.scale.stride, bias, xm.q.rows, (int32_t)c_out, (int32_t)channels, o.dt,
+                         o.m.p, o.m.stride, g.stream);
   });
   return result(o, g.a[7]);
 }
@@ -355,6 +585,12 @@ PyMethodDef g_methods[] = {method<rms_norm<false>, 4>("rms_norm"),
                            method<rms_norm_backward, 5>("rms_norm_backward"),
                            method<matmul_i8, 7>("matmul_i8"),
                            method<sparse_conv_i8, 8>("sparse_conv_i8"),
+                           method<layer_norm, 5>("layer_norm"),
+                           method<layer_norm_backward, 7>("layer_norm_backward"),
+                           method<rotary, 7>("rotary"),
+                           method<quantise_mx4, 1>("quantise_mx4"),
+                           method<dequantise_mx4, 4>("dequantise_mx4"),
+                           method<matmul_mx4, 8>("matmul_mx4"),
                            {"records", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&records)),
                             METH_FASTCALL, nullptr},
                            {"set_error", set_error, METH_O, nullptr},

@@ -12,8 +12,8 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 // CNT consecutive output channels of one row from n on, rounded to T. Rows on 16-byte
 // boundaries (`wide`) are stored past the caches, which keeps the inputs there
 // (16384 x 4096 -> 4096: 230 for 260 us, 124800 x 256 -> 768: 65 for 106 us, in one run).
-template <typename T, int CNT>
-__device__ __forceinline__ void store_run(const ProductArgs& a, i64 row, int n, const float v[CNT], bool wide) {
+template <typename T, int CNT, typename Args>
+__device__ __forceinline__ void store_run(const Args& a, i64 row, int n, const float v[CNT], bool wide) {
   T* out = static_cast<T*>(a.out) + row * a.out_stride + n;
   T r[CNT];
 #pragma unroll

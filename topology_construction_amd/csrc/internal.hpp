@@ -478,7 +478,8 @@ tc_grid_batch* build_pass(const tc_grid_batch* src, int op, const OutAlloc& oa,
 // a flag index outside [0, n_keep) sets the internal-error bit in *flags.
 void mask_leaves(const tc_grid_batch* src, const uint8_t* keep, i64 n_keep, u64* out_mask, int32_t* flags,
                  hipStream_t s);
-// ------------------------------------------------------------------ operators on feature rows (norm.hip, product.hip)
+// ------------------------------------------------------------------ operators on feature rows (norm.hip, product.hip,
+// conv.hip, layer_norm.hip, rotary.hip, mx4.hip, product_mx4.hip)
 struct NormArgs {
   const void* x;
   i64 x_stride;
@@ -537,5 +538,105 @@ struct ProductArgs {
 };
 void product_i8(const ProductArgs& a, hipStream_t s);  // also over a map
 void conv_i8(const ProductArgs& a, hipStream_t s);     // over a map, with rows
+
+struct LayerNormArgs {
+  const void* x;
+  i64 x_stride;
+  const void* residual;  // nullptr: none
+  i64 residual_stride;
+  const void* weight;  // nullptr: ones
+  int weight_dtype;
+  const void* bias;  // nullptr: zeros
+  int bias_dtype;
+  i64 rows;
+  int channels;
+  int dtype;
+  float eps;
+  void* sum;  // nullptr: not wanted
+  void* out;
+  float* mean;  // nullptr: not wanted
+  float* rstd;  // nullptr: not wanted
+};
+void layer_norm(const LayerNormArgs& a, hipStream_t s);
+
+struct LayerNormGradArgs {
+  const void* grad_out;
+  i64 grad_out_stride;
+  const void* grad_sum;  // nullptr: none
+  i64 grad_sum_stride;
+  const void* h;
+  i64 h_stride;
+  const void* weight;  // nullptr: ones
+  int weight_dtype;
+  const float* mean;
+  const float* rstd;
+  i64 rows;
+  int channels;
+  int dtype;
+  void* grad_x;        // nullptr: not wanted
+  float* grad_weight;  // nullptr: not wanted
+  float* grad_bias;    // nullptr: not wanted
+  float* partial;      // layer_norm_grad_workspace bytes, when grad_weight or grad_bias is wanted
+};
+size_t layer_norm_grad_workspace(i64 rows, int channels);
+void layer_norm_grad(const LayerNormGradArgs& a, hipStream_t s);
+
+struct RotaryArgs {
+  const void* x;
+  i64 x_row, x_head;
+  i64 rows;
+  int heads, dim, pairs;
+  int dtype;
+  const int32_t* positions;
+  i64 position_row;
+  int ends[3];  // the pair at which the axis after this one begins; INT32_MAX: none
+  const float* freqs;
+  bool interleaved, inverse;
+  void* out;
+  i64 out_row, out_head;
+  bool in_place;  // out is x, with x's strides
+};
+void rotary(const RotaryArgs& a, hipStream_t s);
+
+struct QuantiseArgs {
+  const void* x;
+  i64 x_stride;
+  i64 rows;
+  int channels;
+  int dtype;
+  uint8_t* q;
+  uint8_t* scale;
+};
+void quantise_mx4(const QuantiseArgs& a, hipStream_t s);
+
+struct DequantiseArgs {
+  const uint8_t* q;
+  i64 q_stride;
+  const uint8_t* scale;
+  i64 scale_stride;
+  i64 rows;
+  int channels;
+  int out_dtype;
+  void* out;
+};
+void dequantise_mx4(const DequantiseArgs& a, hipStream_t s);
+
+struct ProductMx4Args {
+  const uint8_t* x;
+  i64 x_stride;
+  const uint8_t* x_scale;
+  i64 x_scale_stride;
+  const uint8_t* w;
+  i64 w_stride;
+  const uint8_t* w_scale;
+  i64 w_scale_stride;
+  const float* bias;  // nullptr: none
+  i64 rows;
+  int n, k;  // output and input channels
+  int out_dtype;
+  void* out;
+  i64 out_stride;
+};
+void product_mx4(const ProductMx4Args& a, hipStream_t s);
 
 }  // namespace tc
