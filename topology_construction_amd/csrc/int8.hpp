@@ -1,5 +1,5 @@
-// 8-bit rows and weights as the matrix instructions take them: loads, the order
-// in LDS, stores of results (product.hip, conv.hip).
+// 8-bit (and packed 4-bit) rows and weights as the matrix instructions take them: loads, tiles and their order
+// in LDS, stores of results (product.hip, conv.hip, product_mx4.hip).
 #pragma once
 
 #include "rows.hpp"
@@ -86,6 +86,25 @@ __device__ __forceinline__ v4i product_16(v4i w, v4i x, v4i sum) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(w, x, sum, 0, 0, 0);
 }
 
+// The tile of output rows and of output channels: runs of `kGroup` row tiles
+// take all channel tiles before the next run, so that tiles in flight together
+// share rows and weights.
+__device__ __forceinline__ void tile_place(i64 tile, i64 tiles_m, int tiles_n, i64& tm, int& tn) {
+  constexpr int kGroup = 8;
+  const i64 per = (i64)kGroup * tiles_n, g = tile / per, first = g * kGroup;
+  const int size = (int)min((i64)kGroup, tiles_m - first), at = (int)(tile - g * per);
+  tm = first + at % size;
+  tn = at / size;
+}
+
+// Row r of the weights' matrix instruction t of a wave's 64 channels, such that a lane's
+// results of two instructions are 8 consecutive channels and the four lanes of an output
+// row store 64 bytes side by side; and the LDS slot key of such a row.
+__device__ __forceinline__ constexpr int w_row(int t, int r) {
+  return (t >> 1) * 32 + (r >> 2) * 8 + (t & 1) * 4 + (r & 3);
+}
+__device__ __forceinline__ int w_key(int row) { return ((row >> 1) & 1) | ((row >> 2) & 2); }
+
 // This wave's LDS reads and writes are done.
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
@@ -95,5 +114,7 @@ __device__ __forceinline__ void meet() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
+
+__host__ __device__ inline bool aligned_16(const void* p, i64 stride) { return (((uintptr_t)p | (uintptr_t)stride) & 15) == 0; }
 
 }  // namespace tc

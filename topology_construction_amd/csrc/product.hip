@@ -11,25 +11,6 @@ namespace {
 
 // ------------------------------------------------------------------ plain product, many tiles
 
-// The tile of output rows and of output channels: runs of `kGroup` row tiles
-// take all channel tiles before the next run, so that tiles in flight together
-// share rows and weights.
-__device__ __forceinline__ void tile_place(i64 tile, i64 tiles_m, int tiles_n, i64& tm, int& tn) {
-  constexpr int kGroup = 8;
-  const i64 per = (i64)kGroup * tiles_n, g = tile / per, first = g * kGroup;
-  const int size = (int)min((i64)kGroup, tiles_m - first), at = (int)(tile - g * per);
-  tm = first + at % size;
-  tn = at / size;
-}
-
-// Row r of the weights' matrix instruction t of a wave's 64 channels, such that a lane's
-// results of two instructions are 8 consecutive channels and the four lanes of an output
-// row store 64 bytes side by side; and the LDS slot key of such a row.
-__device__ __forceinline__ constexpr int w_row(int t, int r) {
-  return (t >> 1) * 32 + (r >> 2) * 8 + (t & 1) * 4 + (r & 3);
-}
-__device__ __forceinline__ int w_key(int row) { return ((row >> 1) & 1) | ((row >> 2) & 2); }
-
 // BM x BN outputs per workgroup, (BM / WM) * (BN / 64) waves of WM x 64 each, in
 // steps of 64 input channels. kDirect: rows and chunks on 16-byte boundaries go
 // straight into LDS, kBufs - 1 steps ahead of the products, or (kPer = 2, four buffers)
@@ -331,8 +312,6 @@ void launch_few(const ProductArgs& a, hipStream_t s) {
   const i64 blocks = ceil_div(a.rows, kRows * 16) * ceil_div(a.n, kCols * 16);
   launch("k_product_few", k_product_few<T, kRows, kCols>, blocks, kFewWaves * 64, s, a);
 }
-
-bool aligned_16(const void* p, i64 stride) { return (((uintptr_t)p | (uintptr_t)stride) & 15) == 0; }
 
 // The variant of a plain product. Timed at 16384 x 4096 -> 4096 (a), 124800 x 256 -> 768 (b),
 // 2048 x 1024 -> 1024 (c), 100 x 4096 -> 4096 (d), 64 x 1024 -> 1024 (e), bf16 out, in us:
