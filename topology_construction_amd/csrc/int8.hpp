@@ -115,6 +115,4 @@ __device__ __forceinline__ void meet() {
   asm volatile("" ::: "memory");
 }
 
-__host__ __device__ inline bool aligned_16(const void* p, i64 stride) { return (((uintptr_t)p | (uintptr_t)stride) & 15) == 0; }
-
 }  // namespace tc

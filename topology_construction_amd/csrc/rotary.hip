@@ -6,24 +6,16 @@
 // The inverse, by the opposite angle, is also the gradient. Coordinates are any 32-bit integers, so an angle can
 // be 2^31 radians: it is reduced in 64 bits, in turns, where subtracting whole turns is exact. Memory bounds
 // it: a workgroup puts the sines of its rows into LDS once, for all heads, while its rows are under way.
+#include <type_traits>
+
 #include "rows.hpp"
 
 namespace tc {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnits = 4;                        // a thread's units of work
-constexpr int kMaxUnits = kThreads * kUnits;     // a workgroup's
-constexpr int kTableBytes = 16 << 10;            // of sines and cosines in a workgroup
-
-// A quotient by a number below 2^16 of one below 2^16.
-struct Divider {
-  uint32_t by, magic;
-  explicit Divider(uint32_t d) : by(d), magic(d == 1 ? 0 : (uint32_t)((0x100000000ull + d - 1) / d)) {}
-  // n (magic d - 2^32) / 2^32 < n d / 2^32 < 1 is all that the rounding up of magic adds to n
-  __device__ __forceinline__ uint32_t divide(uint32_t n) const { return by == 1 ? n : __umulhi(n, magic); }
-};
+constexpr int kMostThreads = 512;
+constexpr int kTableBytes = 32 << 10;  // of sines and cosines in a workgroup
 
 // cos and sin of p * f radians.
 __device__ __forceinline__ float2 turn_of(int p, float f) {
@@ -42,89 +34,112 @@ __device__ __forceinline__ float2 turn_of(int p, float f) {
   return {(q + 1) & 2 ? -c : c, q & 2 ? -d : d};
 }
 
-struct Plan {
-  i64 rows_each;    // rows of a workgroup
-  int heads_each;   // heads of a workgroup
-  int head_groups;
-  int units;        // of a head's pairs, V pairs each
-  Divider by_units, by_heads;
+// A unit of work is a vector of 16 bytes of firsts of pairs and one of seconds, half the turned channels apart, or two
+// vectors of pairs that are side by side (kNeighbours), or one (kWide). The last unit of a head may have fewer pairs,
+// which go one by one. A thread has the same unit of kDepth rows, all asked for before the sines are made.
+//
+// kWide: outputs on 16-byte boundaries, of which a wave has whole lines, go past the caches: 60000 x 8 x 128 bf16
+// 38 for 53 us, neighbours 40 for 56; 124800 x 16 x 64, neighbours, 110 for 120 (4.7 TB/s). Halves of 64 bytes
+// (124800 x 16 x 64) would take 130 for 115 that way.
+template <typename T, bool kNeighbours, bool kWide>
+struct UnitOf {
+  static constexpr int kVectors = kNeighbours && kWide ? 1 : 2;
+  static constexpr int kPairs = 16 / sizeof(T) * kVectors / 2, kDepth = 8 / kVectors;
 };
 
-// A unit is V pairs: two vectors of 16 bytes, half a head apart or (kNeighbours) side by side. The last
-// unit of a head may have fewer, which go one by one.
-template <typename T, bool kNeighbours>
-__global__ void __launch_bounds__(kThreads) k_rotary(RotaryArgs a, Plan plan) {
-  constexpr int V = 16 / sizeof(T);
-  extern __shared__ float2 s_turn[];  // [rows][pairs]
+struct Plan {
+  int units;        // of a head's pairs
+  int heads_each;   // heads of a workgroup
+  int head_groups;
+  int rows_across;  // rows that the threads of a workgroup are side by side on
+  i64 rows_each;    // rows of a workgroup, at most a thread's times rows_across
+  int pitch;        // pairs of a row of the table, an even number
+};
+
+template <typename T, bool kNeighbours, bool kWide>
+__global__ void __launch_bounds__(kMostThreads) k_rotary(RotaryArgs a, Plan plan) {
+  using U = UnitOf<T, kNeighbours, kWide>;
+  constexpr int V = 16 / sizeof(T), P = U::kPairs, kDepth = U::kDepth, kVectors = U::kVectors;
+  extern __shared__ float2 s_turn[];  // [rows][pitch]
   const i64 row0 = blockIdx.x / plan.head_groups * plan.rows_each;
   const int head0 = blockIdx.x % plan.head_groups * plan.heads_each;
   const int rows = (int)min(plan.rows_each, a.rows - row0), heads = min(plan.heads_each, a.heads - head0);
-  const int units = rows * plan.heads_each * plan.units;
-  const int pairs = a.pairs;
+  const int pairs = a.pairs, tid = threadIdx.x;
+  const int at = tid / plan.units, r0 = at / plan.heads_each, h = at - r0 * plan.heads_each;
+  const int first = (tid - at * plan.units) * P;
+  const int count = r0 < plan.rows_across && h < heads ? min(P, pairs - first) : 0;  // pairs of the unit, 0: none
+  // channels of the first pair; a unit's vectors, and the pairs of one that has fewer, are side by side or `apart`
+  const int c1 = kNeighbours ? 2 * first : first, apart = kNeighbours ? V : pairs;
+  const T* x = static_cast<const T*>(a.x) + (row0 + r0) * a.x_row + (i64)(head0 + h) * a.x_head;
+  T* out = static_cast<T*>(a.out) + (row0 + r0) * a.out_row + (i64)(head0 + h) * a.out_head;
+  auto first_at = [&](int e) { return kNeighbours ? c1 + 2 * e : c1 + e; };
+  auto second_at = [&](int e) { return kNeighbours ? c1 + 2 * e + 1 : c1 + pairs + e; };
+  auto first_of = [](T (&v)[kVectors][V], int e) -> T& { return kNeighbours ? v[2 * e / V][2 * e % V] : v[0][e]; };
+  auto second_of = [](T (&v)[kVectors][V], int e) -> T& { return kNeighbours ? v[2 * e / V][2 * e % V + 1] : v[kVectors - 1][e]; };
 
-  T v[kUnits][2 * V];
-  i64 to[kUnits];
-  int count[kUnits], turn[kUnits], first[kUnits];  // pairs of the unit (0: none), its place in s_turn, its first pair
+  T v[kDepth][kVectors][V];
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int unit = threadIdx.x + i * kThreads;
-    count[i] = 0;
-    if (unit >= units) continue;
-    const int at = plan.by_units.divide(unit), r = plan.by_heads.divide(at), h = at - r * plan.heads_each;
-    if (h >= heads) continue;
-    first[i] = (unit - at * plan.units) * V;
-    count[i] = min(V, pairs - first[i]);
-    turn[i] = r * pairs + first[i];
-    const T* x = static_cast<const T*>(a.x) + (row0 + r) * a.x_row + (i64)(head0 + h) * a.x_head;
-    to[i] = (row0 + r) * a.out_row + (i64)(head0 + h) * a.out_head;
-    if (count[i] == V) {
-      __builtin_memcpy(v[i], x + (kNeighbours ? 2 * first[i] : first[i]), 16);
-      __builtin_memcpy(v[i] + V, x + (kNeighbours ? 2 * first[i] + V : pairs + first[i]), 16);
+  for (int i = 0; i < kDepth; ++i) {
+    if (!count || r0 + i * plan.rows_across >= rows) continue;
+    const T* from = x + i * plan.rows_across * a.x_row;
+    if (count == P) {
+#pragma unroll
+      for (int k = 0; k < kVectors; ++k) __builtin_memcpy(v[i][k], from + c1 + k * apart, 16);
     } else {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (e >= count[i]) continue;
-        v[i][kNeighbours ? 2 * e : e] = x[kNeighbours ? 2 * (first[i] + e) : first[i] + e];
-        v[i][kNeighbours ? 2 * e + 1 : V + e] = x[kNeighbours ? 2 * (first[i] + e) + 1 : pairs + first[i] + e];
-      }
+      for (int e = 0; e < P; ++e)
+        if (e < count) {
+          first_of(v[i], e) = from[first_at(e)];
+          second_of(v[i], e) = from[second_at(e)];
+        }
     }
   }
-  for (int i = threadIdx.x; i < rows * pairs; i += kThreads) {
+  for (int i = tid; i < rows * pairs; i += blockDim.x) {
     const int r = i / pairs, p = i - r * pairs;
     const int axis = (p >= a.ends[0]) + (p >= a.ends[1]) + (p >= a.ends[2]);
     const float2 t = turn_of(a.positions[(row0 + r) * a.position_row + axis], a.freqs[p]);
-    s_turn[i] = {t.x, a.inverse ? -t.y : t.y};
+    s_turn[r * plan.pitch + p] = {t.x, a.inverse ? -t.y : t.y};
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    if (!count[i]) continue;
-    T* out = static_cast<T*>(a.out) + to[i];
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      if (e >= count[i]) continue;
-      const float2 t = s_turn[turn[i] + e];
-      T &p1 = v[i][kNeighbours ? 2 * e : e], &p2 = v[i][kNeighbours ? 2 * e + 1 : V + e];
-      const float x1 = to_f32(p1), x2 = to_f32(p2);
-      p1 = from_f32<T>(fmaf(x1, t.x, -(x2 * t.y)));
-      p2 = from_f32<T>(fmaf(x1, t.y, x2 * t.x));
-    }
-    if (count[i] == V) {
-      __builtin_memcpy(out + (kNeighbours ? 2 * first[i] : first[i]), v[i], 16);
-      __builtin_memcpy(out + (kNeighbours ? 2 * first[i] + V : pairs + first[i]), v[i] + V, 16);
+  for (int i = 0; i < kDepth; ++i) {
+    const int r = r0 + i * plan.rows_across;
+    if (!count || r >= rows) continue;
+    T* to = out + i * plan.rows_across * a.out_row;
+    float2 t[P];
+    if (count == P) {
+      __builtin_memcpy(t, __builtin_assume_aligned(s_turn + r * plan.pitch + first, 16), sizeof(t));
     } else {
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        if (e >= count[i]) continue;
-        out[kNeighbours ? 2 * (first[i] + e) : first[i] + e] = v[i][kNeighbours ? 2 * e : e];
-        out[kNeighbours ? 2 * (first[i] + e) + 1 : pairs + first[i] + e] = v[i][kNeighbours ? 2 * e + 1 : V + e];
+      for (int e = 0; e < P; ++e) t[e] = e < count ? s_turn[r * plan.pitch + first + e] : float2{0.0f, 0.0f};
+    }
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+      T &p1 = first_of(v[i], e), &p2 = second_of(v[i], e);
+      const float x1 = to_f32(p1), x2 = to_f32(p2);
+      p1 = from_f32<T>(fmaf(x1, t[e].x, -(x2 * t[e].y)));
+      p2 = from_f32<T>(fmaf(x1, t[e].y, x2 * t[e].x));
+    }
+    if (count == P) {
+#pragma unroll
+      for (int k = 0; k < kVectors; ++k) {
+        typedef int v4i __attribute__((ext_vector_type(4)));
+        if (kWide) __builtin_nontemporal_store(*reinterpret_cast<const v4i*>(v[i][k]), reinterpret_cast<v4i*>(to + c1 + k * apart));
+        else __builtin_memcpy(to + c1 + k * apart, v[i][k], 16);
       }
+    } else {
+#pragma unroll
+      for (int e = 0; e < P; ++e)
+        if (e < count) {
+          to[first_at(e)] = first_of(v[i], e);
+          to[second_at(e)] = second_of(v[i], e);
+        }
     }
   }
   // what is not turned, into another tensor
   const int rest = a.dim - 2 * pairs;
   if (rest == 0 || a.in_place) return;
-  for (int i = threadIdx.x; i < rows * heads * rest; i += kThreads) {
+  for (int i = tid; i < rows * heads * rest; i += blockDim.x) {
     const int at = i / rest, r = at / heads, h = head0 + at - r * heads, c = 2 * pairs + i - at * rest;
     static_cast<T*>(a.out)[(row0 + r) * a.out_row + h * a.out_head + c] =
         static_cast<const T*>(a.x)[(row0 + r) * a.x_row + h * a.x_head + c];
@@ -137,17 +152,42 @@ void rotary(const RotaryArgs& a, hipStream_t s) {
   if (a.rows == 0 || a.heads == 0) return;
   with_dtype(a.dtype, [&](auto t) {
     using T = decltype(t);
-    constexpr int V = 16 / sizeof(T);
-    const int units = std::max<int>(1, (int)ceil_div(a.pairs, V));
-    // all heads of a row in one workgroup share its sines; rows up to the units of a thread, and to the table's size
-    const int heads_each = std::min(a.heads, std::max(1, kMaxUnits / units));
-    const i64 rows_each = std::max<i64>(1, std::min<i64>({kMaxUnits / ((i64)units * heads_each),
-                                                          kTableBytes / ((i64)sizeof(float2) * std::max(a.pairs, 1)), a.rows}));
-    const int head_groups = (int)ceil_div(a.heads, heads_each);
-    const Plan plan{rows_each, heads_each, head_groups, units, Divider((uint32_t)units), Divider((uint32_t)heads_each)};
-    const size_t lds = sizeof(float2) * (size_t)rows_each * (size_t)a.pairs;
-    launch_lds("k_rotary", a.interleaved ? k_rotary<T, true> : k_rotary<T, false>, ceil_div(a.rows, rows_each) * head_groups,
-               kThreads, lds, s, a, plan);
+    auto go = [&](auto neighbours, auto wide) {
+      using U = UnitOf<T, decltype(neighbours)::value, decltype(wide)::value>;
+      Plan p;
+      p.units = (int)ceil_div(a.pairs, U::kPairs);  // at most kMostThreads: dim is at most 4096
+      // all heads of a row in one workgroup, where they fit, share its sines
+      p.heads_each = std::min(a.heads, kMostThreads / p.units);
+      p.head_groups = (int)ceil_div(a.heads, p.heads_each);
+      p.pitch = a.pairs + a.pairs % 2;
+      // as many rows side by side as leave the fewest lanes of the waves idle
+      const int across = p.heads_each * p.units;
+      const i64 most = std::min<i64>({kMostThreads / across, a.rows,
+                                      std::max(1, kTableBytes / (int)(U::kDepth * sizeof(float2) * p.pitch))});
+      p.rows_across = 1;
+      auto waves = [&](int rows) { return (rows * across + kWave - 1) / kWave; };
+      for (int r = 2; r <= most; ++r)
+        if (r * waves(p.rows_across) >= p.rows_across * waves(r)) p.rows_across = r;
+      // rows for every CU before depth
+      const i64 depth = std::max<i64>(
+          1, std::min<i64>(U::kDepth, a.rows * p.head_groups / (p.rows_across * 2 * (i64)device_cu_count())));
+      p.rows_each = depth * p.rows_across;
+      launch_lds("k_rotary", k_rotary<T, decltype(neighbours)::value, decltype(wide)::value>,
+                 ceil_div(a.rows, p.rows_each) * p.head_groups, waves(p.rows_across) * kWave,
+                 sizeof(float2) * (size_t)p.rows_each * (size_t)p.pitch, s, a, p);
+    };
+    constexpr i64 kSize = sizeof(T);
+    const bool aligned = aligned_16(a.out, (a.out_row | a.out_head) * kSize);
+    if (a.interleaved) {
+      // heads that follow each other, or that are whole lines themselves
+      const i64 turned = 2 * a.pairs * kSize;
+      const bool lines = turned % 128 == 0 || (2 * a.pairs == a.dim && (a.heads == 1 || a.out_head == a.dim));
+      if (aligned && turned % 16 == 0 && turned / 16 <= kMostThreads && lines) go(std::true_type(), std::true_type());
+      else go(std::true_type(), std::false_type());
+    } else {
+      if (aligned && a.pairs * kSize % 128 == 0) go(std::false_type(), std::true_type());
+      else go(std::false_type(), std::false_type());
+    }
   });
 }
 

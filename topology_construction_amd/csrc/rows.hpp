@@ -50,6 +50,9 @@ __device__ __forceinline__ V lanes_reduce(V v, F&& f) {
   return v;
 }
 
+// Whether rows from p on, `stride` bytes apart, begin on 16-byte boundaries.
+__host__ __device__ inline bool aligned_16(const void* p, i64 stride) { return (((uintptr_t)p | (uintptr_t)stride) & 15) == 0; }
+
 // Calls f with a value of the element type that `dtype` names.
 template <typename F>
 inline void with_dtype(int dtype, F&& f) {
