@@ -5,7 +5,6 @@ import torch
 
 from tests import feature_ref
 from tests import token_ref as ref
-from tests.feature_bounds import weight_grad_roundings
 from topology_construction_amd import binding
 
 pytestmark = pytest.mark.gpu
@@ -62,7 +61,7 @@ def _check_grad(got, dy, h, w, mean, rstd, dh, dtype):
     gx, gw, gb = got
     (dx, dw, db), (off, mag_w, mag_b, off_w) = ref.layer_norm_grad(dy, h, w, mean.cpu(), rstd.cpu(), dh, dtype)
     _within(gx, dx, off, "grad_x")
-    n = weight_grad_roundings(h.shape[0]) * ref.U32 * (1 + 2.0 ** -10)
+    n = ref.layer_norm_sum_roundings(h.shape[0]) * ref.U32 * (1 + 2.0 ** -10)
     if gw is not None:
         _within(gw, dw, mag_w * n + off_w, "grad_weight")
     if gb is not None:

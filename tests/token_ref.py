@@ -61,6 +61,13 @@ def layer_norm_grad(grad_out, h, weight, mean, rstd, grad_h, dtype):
     return (dx, (dy * u).sum(0), dy.sum(0)), (bound, (dy * u).abs().sum(0), dy.abs().sum(0), (dy.abs() * off_u).sum(0))
 
 
+def layer_norm_sum_roundings(rows: int) -> int:
+    """Roundings of a term of the weight's or bias's gradient: its two products; the rows of one thread (the rows in at
+    least min(rows, 256) parts); six doublings over a wave, three over its workgroup; 64 slices of at most 1024 parts (16
+    each), by eights, and the eights."""
+    return 2 + -(-rows // 256) + 6 + 3 + 16 + 7 + 7
+
+
 # ------------------------------------------------------------------ rotary positions
 
 

@@ -20,6 +20,10 @@ struct Centre {
   __device__ __forceinline__ float from(float h) const { return (h - hi) - lo; }
 };
 
+// The row stays in registers between the reductions and the outputs. h is stored only after a reduction over the row,
+// when all of x and r is read: it may go over either. The 64-bit additions cost 3 to 7% of the time.
+// Memory bounds it: 16384 x 4096 f16 95 us (5.6 TB/s), f32 205 (5.2), 124800 x 128 bf16 22 (5.9), f32 41 (6.2), one row of
+// 1024 3.3 us.
 template <typename T, int L, int N>
 __global__ void __launch_bounds__(kNormThreads) k_layer_norm(LayerNormArgs a) {
   constexpr int V = Vec<T>::kN;
@@ -98,7 +102,8 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm(LayerNormArgs a) {
 }
 
 // Rows of fewer channels than a vector has (L = 1: one thread a row), or of more than a workgroup's
-// registers hold (L = a workgroup, the row read three times): whole vectors, the rest by elements.
+// registers hold (L = a workgroup, the row read three times): whole vectors, the rest by elements. 2048 x 20000 bf16 166 us
+// for the 66 that its bytes take (weights one by one, three passes), 124800 x 3 f32 5.7.
 template <typename T, int L>
 __global__ void __launch_bounds__(kNormThreads) k_layer_norm_any(LayerNormArgs a) {
   constexpr int V = Vec<T>::kN;
@@ -216,16 +221,21 @@ __device__ __forceinline__ GradSums group_sums(GradSums s, GradScratch& scratch,
   return s;
 }
 
-// (h - m) s of one element. The difference leaves 32 bits for rows beyond half their range, and s
-// is out of the normal range for spreads from 2^126 on: in 64 bits there is room for both.
-template <typename T>
-__device__ __forceinline__ float unit_of(T h, float mean, float rstd) {
-  if constexpr (std::is_same<T, f16>::value) return (to_f32(h) - mean) * rstd;
-  else return (float)(((double)to_f32(h) - (double)mean) * (double)rstd);
-}
+// (h - m) s of a row's elements. The difference leaves 32 bits for rows beyond half their range, s the normal
+// numbers for spreads from 2^126 on: a power of two, 1 but for such rows and for tiny ones, goes from one to the other.
+struct Unit {
+  float by, centre, rstd;
+  __device__ __forceinline__ Unit(float mean, float s) {
+    by = s < 0x1p-62f ? 0x1p-64f : s > 0x1p62f ? 0x1p64f : 1.0f;
+    centre = -(mean * by);
+    rstd = s * (s < 0x1p-62f ? 0x1p64f : s > 0x1p62f ? 0x1p-64f : 1.0f);
+  }
+  __device__ __forceinline__ float of(float h) const { return fmaf(h, by, centre) * rstd; }
+};
 
 // This workgroup's parts of dw = sum dy u and of db = sum dy: each thread adds up its channels over its rows
-// in registers, the workgroup's groups are joined once at the end.
+// in registers, the workgroup's groups are joined once at the end. 16384 x 4096 f16 115 us (4.7 TB/s) and 6 for the sum of
+// the parts, f32 205 and 8, 124800 x 128 bf16 23 and 4.
 template <typename T, int L, int N, bool kParams>
 __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad(LayerNormGradArgs a) {
   constexpr int V = Vec<T>::kN;
@@ -259,7 +269,8 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad(LayerNormGradA
       h[j] = next_h[j];
       dh[j] = next_dh[j];
     }
-    const float mean = next_mean, rstd = next_rstd;
+    const float rstd = next_rstd;
+    const Unit unit(next_mean, rstd);
     ask(row + step);
     GradSums s{0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -267,7 +278,7 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad(LayerNormGradA
       if (at.c[j] < 0) continue;
 #pragma unroll
       for (int e = 0; e < V; ++e)
-        if (!at.ragged || e >= at.skip[j]) s.add(to_f32(dy[j].v[e]) * w[j][e], unit_of(h[j].v[e], mean, rstd));
+        if (!at.ragged || e >= at.skip[j]) s.add(to_f32(dy[j].v[e]) * w[j][e], unit.of(to_f32(h[j].v[e])));
     }
     s = group_sums<L>(s, s_red, turn);
     s.finish((float)a.channels);
@@ -278,7 +289,7 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad(LayerNormGradA
       Vec<T> o;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float y = to_f32(dy[j].v[e]), u = unit_of(h[j].v[e], mean, rstd) - s.v;
+        const float y = to_f32(dy[j].v[e]), u = unit.of(to_f32(h[j].v[e])) - s.v;
         if constexpr (kParams) {
           dw[j][e] += y * u;
           db[j][e] += y;
@@ -333,7 +344,7 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad(LayerNormGradA
   }
 }
 
-// Rows of fewer channels than a vector has, one thread a row.
+// Rows of fewer channels than a vector has, one thread a row: 124800 x 3 f32 8 us with the sum.
 template <typename T, bool kParams>
 __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad_narrow(LayerNormGradArgs a) {
   constexpr int C = Vec<T>::kN - 1;  // the most channels
@@ -347,14 +358,15 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad_narrow(LayerNo
     const T* dy = static_cast<const T*>(a.grad_out) + row * a.grad_out_stride;
     const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
     const T* dh = a.grad_sum ? static_cast<const T*>(a.grad_sum) + row * a.grad_sum_stride : nullptr;
-    const float mean = a.mean[row], rstd = a.rstd[row];
+    const float rstd = a.rstd[row];
+    const Unit unit(a.mean[row], rstd);
     float y[C], v[C];
     GradSums s{0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       if (c >= a.channels) continue;
       y[c] = to_f32(dy[c]);
-      v[c] = unit_of(h[c], mean, rstd);
+      v[c] = unit.of(to_f32(h[c]));
       s.add(y[c] * w[c], v[c]);
     }
     s.finish((float)a.channels);
@@ -391,7 +403,7 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad_narrow(LayerNo
 }
 
 // Rows that a workgroup's registers do not hold: a workgroup a row, the row read twice; mean(v), which the
-// parts of dw need, is left for k_layer_norm_grad_part.
+// parts of dw need, is left for k_layer_norm_grad_part (which reads both once more): 2048 x 20000 bf16 333 us together.
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad_wide(LayerNormGradArgs a, float* unit_mean) {
   constexpr int V = Vec<T>::kN;
@@ -402,7 +414,8 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad_wide(LayerNorm
     const T* dy = static_cast<const T*>(a.grad_out) + row * a.grad_out_stride;
     const T* h = static_cast<const T*>(a.h) + row * a.h_stride;
     const T* dh = a.grad_sum ? static_cast<const T*>(a.grad_sum) + row * a.grad_sum_stride : nullptr;
-    const float mean = a.mean[row], rstd = a.rstd[row];
+    const float rstd = a.rstd[row];
+    const Unit unit(a.mean[row], rstd);
     auto each = [&](auto&& f) {
       for (int c = threadIdx.x * V; c < whole; c += kNormThreads * V) {
         Vec<T> y, v;
@@ -417,7 +430,7 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad_wide(LayerNorm
     GradSums s{0.0f, 0.0f, 0.0f};
     each([&](const T* y, const T* v, int c, auto n) {
 #pragma unroll
-      for (int e = 0; e < n; ++e) s.add(to_f32(y[e]) * weight(c + e), unit_of(v[e], mean, rstd));
+      for (int e = 0; e < n; ++e) s.add(to_f32(y[e]) * weight(c + e), unit.of(to_f32(v[e])));
     });
     s = group_sums<kNormThreads>(s, s_red, turn);
     s.finish((float)a.channels);
@@ -429,7 +442,7 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad_wide(LayerNorm
       if (dh) __builtin_memcpy(add, dh + c, n * sizeof(T));
 #pragma unroll
       for (int e = 0; e < n; ++e) {
-        const float u = unit_of(v[e], mean, rstd) - s.v;
+        const float u = unit.of(to_f32(v[e])) - s.v;
         const float d = rstd * ((to_f32(y[e]) * weight(c + e) - s.g) - u * s.gv);
         o[e] = from_f32<T>(dh ? d + to_f32(add[e]) : d);
       }
@@ -449,32 +462,39 @@ __global__ void __launch_bounds__(kNormThreads)
   for (i64 row = r0; row < r1; ++row) {
     const float y = to_f32(static_cast<const T*>(a.grad_out)[row * a.grad_out_stride + c]);
     const T h = static_cast<const T*>(a.h)[row * a.h_stride + c];
-    dw += y * (unit_of(h, a.mean[row], a.rstd[row]) - unit_mean[row]);
+    dw += y * (Unit(a.mean[row], a.rstd[row]).of(to_f32(h)) - unit_mean[row]);
     db += y;
   }
   a.partial[(i64)part * 2 * a.channels + c] = dw;
   a.partial[((i64)part * 2 + 1) * a.channels + c] = db;
 }
 
-// dw and db: the sums of the parts, 32 channels by 32 slices of the parts a workgroup.
-constexpr int kSumChannels = 32, kSumSlices = 32;
+// dw and db: the sums of the parts, 16 channels by 64 slices of the parts a workgroup, the slices by eights.
+constexpr int kSumChannels = 16, kSumSlices = 64, kSumFirst = 8;
 __global__ void __launch_bounds__(kSumChannels* kSumSlices)
     k_layer_norm_grad_sum(const float* partial, int parts, int channels, float* dw, float* db) {
-  __shared__ float s_part[kSumSlices][kSumChannels];
+  __shared__ float s_part[kSumSlices][kSumChannels], s_first[kSumFirst][kSumChannels];
   const int cl = threadIdx.x % kSumChannels, slice = threadIdx.x / kSumChannels;
   const i64 c = (i64)blockIdx.x * kSumChannels + cl;  // of both, one after the other
   const bool bias = c >= channels;
   float* out = bias ? db : dw;
   float acc = 0.0f;
   if (c < 2 * (i64)channels) {
-#pragma unroll 8
+#pragma unroll 16
     for (int p = slice; p < parts; p += kSumSlices) acc += partial[(i64)p * 2 * channels + c];
   }
   s_part[slice][cl] = acc;
   __syncthreads();
+  if (slice < kSumFirst) {
+    acc = s_part[slice * kSumFirst][cl];
+#pragma unroll
+    for (int k = 1; k < kSumSlices / kSumFirst; ++k) acc += s_part[slice * kSumFirst + k][cl];
+    s_first[slice][cl] = acc;
+  }
+  __syncthreads();
   if (slice == 0 && c < 2 * (i64)channels && out) {
 #pragma unroll
-    for (int k = 1; k < kSumSlices; ++k) acc += s_part[k][cl];
+    for (int k = 1; k < kSumFirst; ++k) acc += s_first[k][cl];
     out[bias ? c - channels : c] = acc;
   }
 }
@@ -482,6 +502,14 @@ __global__ void __launch_bounds__(kSumChannels* kSumSlices)
 // Workgroups whose parts of the weights' gradients are joined at the end.
 constexpr int kGradParts = 1024;
 int grad_parts(i64 rows) { return (int)std::max<i64>(1, std::min<i64>(rows, kGradParts)); }
+
+// Workgroups a CU that k_layer_norm_grad's registers leave room for, and no more than four: as many parts are one round, with
+// the least traffic of the parts themselves (16384 x 4096 f16: 121 us, in 1024 parts 127; 8192 x 8192 bf16 128, 155;
+// 8192 x 8192 f32 216, 242).
+template <typename T>
+int resident(int vectors) {
+  return vectors >= 8 ? 1 : vectors >= 4 ? 2 : vectors == 2 && sizeof(T) == 2 ? 3 : 4;
+}
 
 // The most channels that the registers of a workgroup hold for every type: wider rows may need a
 // float each in the workspace.
@@ -529,7 +557,8 @@ void layer_norm_grad(const LayerNormGradArgs& a, hipStream_t s) {
                  constexpr int L = decltype(l)::value, N = decltype(n)::value;
                  const i64 groups = ceil_div(a.rows, kNormThreads / L);
                  if (params) {
-                   parts = (int)std::min<i64>(parts, groups);
+                   const i64 most_parts = resident<T>(N) * (i64)device_cu_count();
+                   parts = (int)std::min<i64>({parts, groups, most_parts});
                    launch("k_layer_norm_grad", k_layer_norm_grad<T, L, N, true>, parts, kNormThreads, s, a);
                  } else {
                    launch("k_layer_norm_grad", k_layer_norm_grad<T, L, N, false>, std::min(groups, most), kNormThreads,
