@@ -221,14 +221,15 @@ __device__ __forceinline__ GradSums group_sums(GradSums s, GradScratch& scratch,
   return s;
 }
 
-// (h - m) s of a row's elements. The difference leaves 32 bits for rows beyond half their range, s the normal
-// numbers for spreads from 2^126 on: a power of two, 1 but for such rows and for tiny ones, goes from one to the other.
+// (h - m) s of a row's elements. The difference leaves 32 bits for rows beyond half their range, and s the normal
+// numbers for spreads from 2^126 on: a power of two, 1 but for rows of such sizes, goes from one to the other.
 struct Unit {
   float by, centre, rstd;
   __device__ __forceinline__ Unit(float mean, float s) {
-    by = s < 0x1p-62f ? 0x1p-64f : s > 0x1p62f ? 0x1p64f : 1.0f;
+    const bool large = s < 0x1p-62f;
+    by = large ? 0x1p-64f : 1.0f;
     centre = -(mean * by);
-    rstd = s * (s < 0x1p-62f ? 0x1p64f : s > 0x1p62f ? 0x1p-64f : 1.0f);
+    rstd = s * (large ? 0x1p64f : 1.0f);
   }
   __device__ __forceinline__ float of(float h) const { return fmaf(h, by, centre) * rstd; }
 };
