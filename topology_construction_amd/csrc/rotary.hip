@@ -162,15 +162,16 @@ void rotary(const RotaryArgs& a, hipStream_t s) {
       p.pitch = a.pairs + a.pairs % 2;
       // as many rows side by side as leave the fewest lanes of the waves idle
       const int across = p.heads_each * p.units;
-      const i64 most = std::min<i64>({kMostThreads / across, a.rows,
-                                      std::max(1, kTableBytes / (int)(U::kDepth * sizeof(float2) * p.pitch))});
+      const i64 table_rows = std::max<i64>(1, kTableBytes / ((i64)sizeof(float2) * p.pitch));
+      const i64 most = std::min<i64>({kMostThreads / across, a.rows, std::max<i64>(1, table_rows / U::kDepth)});
       p.rows_across = 1;
       auto waves = [&](int rows) { return (rows * across + kWave - 1) / kWave; };
       for (int r = 2; r <= most; ++r)
         if (r * waves(p.rows_across) >= p.rows_across * waves(r)) p.rows_across = r;
       // rows for every CU before depth
       const i64 depth = std::max<i64>(
-          1, std::min<i64>(U::kDepth, a.rows * p.head_groups / (p.rows_across * 2 * (i64)device_cu_count())));
+          1, std::min<i64>({U::kDepth, table_rows / p.rows_across,
+                            a.rows * p.head_groups / (p.rows_across * 2 * (i64)device_cu_count())}));
       p.rows_each = depth * p.rows_across;
       launch_lds("k_rotary", k_rotary<T, decltype(neighbours)::value, decltype(wide)::value>,
                  ceil_div(a.rows, p.rows_each) * p.head_groups, waves(p.rows_across) * kWave,
