@@ -314,7 +314,8 @@ def test_rotary_empty_and_refusals():
                       (lambda: binding.tc_rotary(x, pos, freqs, (9, -1)), ValueError), (lambda: binding.tc_rotary(x, pos, freqs, (2 ** 70, 1)), ValueError),
                       (lambda: binding.tc_rotary(x, pos, freqs, (4.0, 4)), TypeError), (lambda: binding.tc_rotary(x[..., :14], pos, freqs, (4, 4)), binding.TopoError),
                       (lambda: binding.tc_rotary(x[..., ::2], pos, freqs[:4], (2, 2)), ValueError), (lambda: binding.tc_rotary(x[0, 0], pos, freqs, (4, 4)), ValueError),
-                      (lambda: binding.tc_rotary(x, pos, freqs, (4, 4), out=x[:1].expand(4, 2, 16)), binding.TopoError),
+                      (lambda: binding.tc_rotary(x, pos, freqs, (4, 4), out=x[:1].clone().expand(4, 2, 16)), binding.TopoError),
+                      (lambda: binding.tc_rotary(x, pos, freqs, (4, 4), out=x[:1].expand(4, 2, 16)), ValueError),
                       (lambda: binding.tc_rotary(x, pos, freqs, (4, 4), out=x[:3]), ValueError), (lambda: binding.tc_rotary(x, pos, freqs, (4, 4), out=x.half()), TypeError),
                       (lambda: binding.tc_rotary(x, pos, freqs.clone().requires_grad_(), (4, 4)), ValueError),
                       (lambda: binding.tc_rotary(x, pos, freqs, (4, 4), out=x.clone().requires_grad_()), ValueError),

@@ -765,7 +765,8 @@ def tc_rotary(x, positions, freqs, sections=None, interleaved: bool = False, inv
         if stream is not None:  # as tc_rms_norm
             with ops.on_stream(stream):
                 return tc_rotary(x, positions, freqs, sections, interleaved, inverse)
-        return ops.rotary_function(x, positions, freqs, sections, interleaved, inverse)
+        return ops.rotary_function(x, positions, freqs, sections if sections is None else tuple(sections), interleaved,
+                                   inverse)
     return ops.call(ops.rotary, stream, x, positions, freqs, sections, interleaved, inverse, out)
 
 
@@ -786,7 +787,8 @@ def tc_dequantise_mx4(q, scale, channels=None, out_dtype=None, stream=None):
 
 def tc_matmul_mx4(x, x_scale, w, w_scale, channels=None, bias=None, out_dtype=None, out=None, stream=None):
     """Product of 4-bit rows (x, x_scale) with 4-bit weights (w, w_scale), both as tc_quantise_mx4 lays them out, [rows, c_in]
-    and [c_out, c_in]; `channels` is c_in, needed where it is odd. float32 bias [c_out]; output as for tc_matmul_i8."""
+    and [c_out, c_in]; `channels` is c_in, needed where it is odd. float32 bias [c_out]; output as for tc_matmul_i8. Nothing
+    is recorded for a gradient."""
     ops = _ops()
     return ops.call(ops.matmul_mx4, stream, x, x_scale, w, w_scale, channels, bias, out_dtype, out)
 

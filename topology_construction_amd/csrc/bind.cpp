@@ -5,6 +5,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/MemoryOverlap.h>
 #include <c10/core/GradMode.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -364,6 +365,11 @@ PyObject* rotary(const Args& g) {
       bad_value("out requires a gradient, which this call has none for");
     if (out.sizes() != x.sizes()) bad_value("out has another shape than x");
     o = heads_of(out, "out", type, device);
+    // x itself, or apart from it (strided parts of one tensor are the caller's to keep apart)
+    const bool same = o.p == h.p && (h.rows < 2 || o.row == h.row) && (h.heads < 2 || o.head == h.head);
+    if (x.numel() > 0 && !same &&
+        (o.p == h.p || at::get_overlap_status(x, out) == at::MemOverlapStatus::Partial))
+      bad_value("out overlaps x without being x");
   }
   if (h.heads > 0)
     unlocked([&]() {
