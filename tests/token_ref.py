@@ -63,9 +63,9 @@ def layer_norm_grad(grad_out, h, weight, mean, rstd, grad_h, dtype):
 
 def layer_norm_sum_roundings(rows: int) -> int:
     """Roundings of a term of the weight's or bias's gradient: its two products; the rows of one thread (the rows in at
-    least min(rows, 256) parts); six doublings over a wave, three over its workgroup; 64 slices of at most 1024 parts (16
+    least min(rows, 256) parts); six doublings over a wave, three over its workgroup; 32 slices of at most 1024 parts (32
     each), by eights, and the eights."""
-    return 2 + -(-rows // 256) + 6 + 3 + 16 + 7 + 7
+    return 2 + -(-rows // 256) + 6 + 3 + 32 + 7 + 3
 
 
 # ------------------------------------------------------------------ rotary positions
