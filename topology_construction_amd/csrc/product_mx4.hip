@@ -73,16 +73,14 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
 
   // this lane's part of each load: a row of x or of w, one chunk of it
   const Buffer xb = buffer_at(x0), wb = buffer_at(w0);
-  unsigned at[kLoads];         // kDirect
-  const int8_t* from[kLoads];  // otherwise
-  v4i held[kLoads];
+  unsigned at[kLoads];  // kDirect
+  v4i held[kLoads];     // otherwise
   const int chunk = (lane & 3) ^ slot_key(lane >> 2);  // the same for all loads, whose rows begin at multiples of 16
 #pragma unroll
   for (int i = 0; i < kLoads; ++i) {
     const int part = (wave * kLoads + i) * 16, r = part + (lane >> 2);
     const i64 row = part < BM ? min((i64)r, a.rows - 1 - row0) : min(r - BM, a.n - 1 - n0);
-    if (kDirect) at[i] = (unsigned)row * (unsigned)(part < BM ? a.x_stride : a.w_stride) + chunk * 16;
-    else from[i] = part < BM ? x0 + row * a.x_stride : w0 + row * a.w_stride;
+    at[i] = (unsigned)row * (unsigned)(part < BM ? a.x_stride : a.w_stride) + chunk * 16;
   }
   const int steps = (a.k + 127) / 128;
   auto issue = [&](int step) {
@@ -92,15 +90,20 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
     for (int i = 0; i < kLoads; ++i)
       load_to_lds((wave * kLoads + i) * 16 < BM ? xb : wb, have ? at[i] : kOutside, step * 64, to + i * 1024);
   };
+  // the largest tile makes its addresses anew for every step: kept, they take registers that it has not
+  constexpr bool kAnew = WM * WN >= 128 * 64;
   auto load = [&](int step) {
     if (step >= steps) return;
-    if ((step + 1) * 128 <= a.k) {
+    int l = lane;
+    if constexpr (kAnew) asm volatile("" : "+v"(l));
+    const int c = step * 64 + ((l & 3) ^ slot_key(l >> 2)) * 16;
 #pragma unroll
-      for (int i = 0; i < kLoads; ++i) __builtin_memcpy(&held[i], from[i] + step * 64 + chunk * 16, 16);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kLoads; ++i)
-        held[i] = load_32_tail(reinterpret_cast<const uint8_t*>(from[i]), step * 64 + chunk * 16, a.k);
+    for (int i = 0; i < kLoads; ++i) {
+      const int part = (wave * kLoads + i) * 16, r = part + (l >> 2);
+      const int8_t* const from = part < BM ? x0 + min((i64)r, a.rows - 1 - row0) * a.x_stride
+                                           : w0 + (i64)min(r - BM, a.n - 1 - n0) * a.w_stride;
+      if ((step + 1) * 128 <= a.k) __builtin_memcpy(&held[i], from + c, 16);
+      else held[i] = load_32_tail(reinterpret_cast<const uint8_t*>(from), c, a.k);
     }
   };
   auto put = [&](int step) {
@@ -111,32 +114,28 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
   };
 
   // exponents: this thread's pieces of rows of the tile, x's rows first; in LDS first those of all rows' first four steps
-  const int8_t* scale_from[kScales];
   v4i scale_held[kScales];
   const int blocks = (a.k + 31) / 32, piece = tid & 1;
-#pragma unroll
-  for (int i = 0; i < kScales; ++i) {
-    const int r = (tid + i * kThreads) / 2;
-    scale_from[i] = reinterpret_cast<const int8_t*>(
-        r < BM ? a.x_scale + min(row0 + r, a.rows - 1) * a.x_scale_stride
-               : a.w_scale + (i64)min(n0 + r - BM, a.n - 1) * a.w_scale_stride);
-  }
   auto load_scales = [&](int eight) {
     if (eight * 8 >= steps) return;
-    const int first = eight * 32 + piece * 16;
+    int t = tid;
+    if constexpr (kAnew) asm volatile("" : "+v"(t));
+    const int first = eight * 32 + (t & 1) * 16;
 #pragma unroll
     for (int i = 0; i < kScales; ++i) {
+      const int r = (t + i * kThreads) / 2;
+      const uint8_t* const at = first + (r < BM ? a.x_scale + min(row0 + r, a.rows - 1) * a.x_scale_stride
+                                                : a.w_scale + (i64)min(n0 + r - BM, a.n - 1) * a.w_scale_stride);
       if ((eight + 1) * 32 <= blocks) {
-        __builtin_memcpy(&scale_held[i], scale_from[i] + first, 16);
+        __builtin_memcpy(&scale_held[i], at, 16);
       } else {  // zeros beyond the last
-        const int8_t* const at = scale_from[i] + first;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int left = blocks - first - e * 4;
           int v = 0;
           if (left >= 4) __builtin_memcpy(&v, at + e * 4, 4);
           else
-            for (int k = 0; k < left; ++k) v |= (int)(uint8_t)at[e * 4 + k] << (8 * k);
+            for (int k = 0; k < left; ++k) v |= (int)at[e * 4 + k] << (8 * k);
           scale_held[i][e] = v;
         }
       }
@@ -428,7 +427,7 @@ void launch_tile(const ProductMx4Args& a, hipStream_t s) {
 // The variant, and what others took (us, bf16 out, captured launches one after another):
 //   rows x c_in -> c_out       256x256  128x128  64x64  256x128, all steps at once   32x32  16x16 (few)
 //   16384 x 4096 -> 4096           165      204    300
-//   16384 x 4095 -> 4096           177      222    334   (through registers)
+//   16384 x 4095 -> 4096           186      222    334   (through registers)
 //   3000 x 4096 -> 4096           34.5     47.1   60.0
 //   2048 x 4096 -> 4096           30.4     26.9   42.1
 //   2500 x 2048 -> 2048           18.6     13.7   16.1
