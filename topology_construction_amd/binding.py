@@ -5,7 +5,7 @@ module only converts torch tensors to device pointers, passes torch's current
 stream, supplies torch's caching allocator for the output buffers and wraps the
 results as torch tensor views. It never computes topology itself and raises
 when the library is missing. The operators on feature rows (tc_rms_norm,
-tc_matmul_i8, tc_sparse_conv_i8, ...) take and return torch tensors directly,
+tc_matmul_i8, tc_sparse_conv_i8, tc_layer_norm, tc_rotary, tc_matmul_mx4, ...) take and return torch tensors directly,
 through ``_features.so`` (csrc/bind.cpp).
 
 Function names follow the C ABI (tc_batch_from_ijk, tc_build_batched_topology,
@@ -681,7 +681,8 @@ def tc_rms_norm(x, weight=None, residual=None, eps: float = 1e-6, stream=None):
     out = h * s * weight. Returns (out, h, rstd): h is x itself without a residual,
     rstd float32 [rows] is s, kept for tc_rms_norm_backward. Where autograd records (x, weight
     or residual requires a gradient), out and h carry the graph; rstd never does, and there
-    are no second derivatives and no forward-mode tangents. The other operators here record nothing."""
+    are no second derivatives and no forward-mode tangents. tc_layer_norm and tc_rotary are recorded too; the other
+    operators here record nothing."""
     ops = _ops()
     if ops.records(x, weight, residual):
         if stream is not None:  # the backward runs on the stream that the forward was recorded on
