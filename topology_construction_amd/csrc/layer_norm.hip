@@ -20,6 +20,22 @@ struct Centre {
   __device__ __forceinline__ float from(float h) const { return (h - hi) - lo; }
 };
 
+// The weights of N channels from c on (T's type, or 32 bits; `none` without any).
+template <typename T, int N>
+__device__ __forceinline__ void weights_at(float (&w)[N], const void* p, int dtype, int c, float none) {
+  if (!p) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] = none;
+  } else if (dtype == TC_F32) {
+    __builtin_memcpy(w, static_cast<const float*>(p) + c, sizeof(w));
+  } else {
+    T t[N];
+    __builtin_memcpy(t, static_cast<const T*>(p) + c, sizeof(t));
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] = to_f32(t[e]);
+  }
+}
+
 // The row stays in registers between the reductions and the outputs. h is stored only after a reduction over the row,
 // when all of x and r is read: it may go over either. The 64-bit additions cost 3 to 7% of the time.
 // Memory bounds it: 16384 x 4096 f16 95 us (5.6 TB/s), f32 205 (5.2), 124800 x 128 bf16 22 (5.9), f32 41 (6.2), one row of
@@ -102,8 +118,8 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm(LayerNormArgs a) {
 }
 
 // Rows of fewer channels than a vector has (L = 1: one thread a row), or of more than a workgroup's
-// registers hold (L = a workgroup, the row read three times): whole vectors, the rest by elements. 2048 x 20000 bf16 166 us
-// for the 66 that its bytes take (weights one by one, three passes), 124800 x 3 f32 5.7.
+// registers hold (L = a workgroup, the row read three times): whole vectors, the rest by elements. 2048 x 20000 bf16 97 us
+// for the 65 that its bytes take (weights one by one: 166), 124800 x 3 f32 5.4.
 template <typename T, int L>
 __global__ void __launch_bounds__(kNormThreads) k_layer_norm_any(LayerNormArgs a) {
   constexpr int V = Vec<T>::kN;
@@ -165,12 +181,14 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm_any(LayerNormArgs a
     }
     each(sum, [&](const T* v, int c, auto n) {
       T o[n];
+      float w[n], b[n];
+      weights_at<T, n>(w, a.weight, a.weight_dtype, c, 1.0f);
+      weights_at<T, n>(b, a.bias, a.bias_dtype, c, 0.0f);
 #pragma unroll
       for (int e = 0; e < n; ++e) {
         const float f = to_f32(v[e]);
         const float u = again ? (float)ldexp((double)f - mean, s.shift) * s.root : m.from(f) * s.root;
-        o[e] = from_f32<T>(fmaf(u, a.weight ? weight_at(a.weight, a.weight_dtype, c + e) : 1.0f,
-                                a.bias ? weight_at(a.bias, a.bias_dtype, c + e) : 0.0f));
+        o[e] = from_f32<T>(fmaf(u, w[e], b[e]));
       }
       __builtin_memcpy(out + c, o, n * sizeof(T));
     });
@@ -404,7 +422,8 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad_narrow(LayerNo
 }
 
 // Rows that a workgroup's registers do not hold: a workgroup a row, the row read twice; mean(v), which the
-// parts of dw need, is left for k_layer_norm_grad_part (which reads both once more): 2048 x 20000 bf16 333 us together.
+// parts of dw need, is left for k_layer_norm_grad_part (which reads both once more): 2048 x 20000 bf16 206 us
+// together (weights one by one: 333).
 template <typename T>
 __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad_wide(LayerNormGradArgs a, float* unit_mean) {
   constexpr int V = Vec<T>::kN;
@@ -427,11 +446,12 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad_wide(LayerNorm
       for (int c = whole + threadIdx.x; c < a.channels; c += kNormThreads)
         f(dy + c, h + c, c, std::integral_constant<int, 1>());
     };
-    auto weight = [&](int c) { return a.weight ? weight_at(a.weight, a.weight_dtype, c) : 1.0f; };
     GradSums s{0.0f, 0.0f, 0.0f};
     each([&](const T* y, const T* v, int c, auto n) {
+      float w[n];
+      weights_at<T, n>(w, a.weight, a.weight_dtype, c, 1.0f);
 #pragma unroll
-      for (int e = 0; e < n; ++e) s.add(to_f32(y[e]) * weight(c + e), unit.of(to_f32(v[e])));
+      for (int e = 0; e < n; ++e) s.add(to_f32(y[e]) * w[e], unit.of(to_f32(v[e])));
     });
     s = group_sums<kNormThreads>(s, s_red, turn);
     s.finish((float)a.channels);
@@ -440,11 +460,13 @@ __global__ void __launch_bounds__(kNormThreads) k_layer_norm_grad_wide(LayerNorm
     T* dx = static_cast<T*>(a.grad_x) + row * a.channels;
     each([&](const T* y, const T* v, int c, auto n) {
       T o[n], add[n];
+      float w[n];
+      weights_at<T, n>(w, a.weight, a.weight_dtype, c, 1.0f);
       if (dh) __builtin_memcpy(add, dh + c, n * sizeof(T));
 #pragma unroll
       for (int e = 0; e < n; ++e) {
         const float u = unit.of(to_f32(v[e])) - s.v;
-        const float d = rstd * ((to_f32(y[e]) * weight(c + e) - s.g) - u * s.gv);
+        const float d = rstd * ((to_f32(y[e]) * w[e] - s.g) - u * s.gv);
         o[e] = from_f32<T>(dh ? d + to_f32(add[e]) : d);
       }
       __builtin_memcpy(dx + c, o, n * sizeof(T));
