@@ -90,20 +90,30 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
     for (int i = 0; i < kLoads; ++i)
       load_to_lds((wave * kLoads + i) * 16 < BM ? xb : wb, have ? at[i] : kOutside, step * 64, to + i * 1024);
   };
-  // the largest tile makes its addresses anew for every step: kept, they take registers that it has not
+  // through registers: the rows of this lane's loads; the largest tile makes them anew for every step, since kept they take
+  // registers that it has not (it would use scratch memory)
   constexpr bool kAnew = WM * WN >= 128 * 64;
+  auto row_of = [&](int i, int lane) {
+    const int part = (wave * kLoads + i) * 16, r = part + (lane >> 2);
+    return part < BM ? x0 + min((i64)r, a.rows - 1 - row0) * a.x_stride : w0 + (i64)min(r - BM, a.n - 1 - n0) * a.w_stride;
+  };
+  const int8_t* from[kLoads];
+  if constexpr (!kDirect && !kAnew) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) from[i] = row_of(i, lane);
+  }
   auto load = [&](int step) {
     if (step >= steps) return;
     int l = lane;
     if constexpr (kAnew) asm volatile("" : "+v"(l));
-    const int c = step * 64 + ((l & 3) ^ slot_key(l >> 2)) * 16;
+    const int c = step * 64 + (kAnew ? (l & 3) ^ slot_key(l >> 2) : chunk) * 16;
+    if ((step + 1) * 128 <= a.k) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int part = (wave * kLoads + i) * 16, r = part + (l >> 2);
-      const int8_t* const from = part < BM ? x0 + min((i64)r, a.rows - 1 - row0) * a.x_stride
-                                           : w0 + (i64)min(r - BM, a.n - 1 - n0) * a.w_stride;
-      if ((step + 1) * 128 <= a.k) __builtin_memcpy(&held[i], from + c, 16);
-      else held[i] = load_32_tail(reinterpret_cast<const uint8_t*>(from), c, a.k);
+      for (int i = 0; i < kLoads; ++i) __builtin_memcpy(&held[i], (kAnew ? row_of(i, l) : from[i]) + c, 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kLoads; ++i)
+        held[i] = load_32_tail(reinterpret_cast<const uint8_t*>(kAnew ? row_of(i, l) : from[i]), c, a.k);
     }
   };
   auto put = [&](int step) {
@@ -116,29 +126,37 @@ __global__ void __launch_bounds__((BM / WM) * (BN / WN) * 64)
   // exponents: this thread's pieces of rows of the tile, x's rows first; in LDS first those of all rows' first four steps
   v4i scale_held[kScales];
   const int blocks = (a.k + 31) / 32, piece = tid & 1;
+  auto scales_of = [&](int i, int tid) {
+    const int r = (tid + i * kThreads) / 2;
+    return r < BM ? a.x_scale + min(row0 + r, a.rows - 1) * a.x_scale_stride
+                  : a.w_scale + (i64)min(n0 + r - BM, a.n - 1) * a.w_scale_stride;
+  };
+  const uint8_t* scale_from[kScales];
+  if constexpr (!kAnew) {
+#pragma unroll
+    for (int i = 0; i < kScales; ++i) scale_from[i] = scales_of(i, tid);
+  }
   auto load_scales = [&](int eight) {
     if (eight * 8 >= steps) return;
     int t = tid;
     if constexpr (kAnew) asm volatile("" : "+v"(t));
     const int first = eight * 32 + (t & 1) * 16;
+    auto at = [&](int i) { return first + (kAnew ? scales_of(i, t) : scale_from[i]); };
+    if ((eight + 1) * 32 <= blocks) {
 #pragma unroll
-    for (int i = 0; i < kScales; ++i) {
-      const int r = (t + i * kThreads) / 2;
-      const uint8_t* const at = first + (r < BM ? a.x_scale + min(row0 + r, a.rows - 1) * a.x_scale_stride
-                                                : a.w_scale + (i64)min(n0 + r - BM, a.n - 1) * a.w_scale_stride);
-      if ((eight + 1) * 32 <= blocks) {
-        __builtin_memcpy(&scale_held[i], at, 16);
-      } else {  // zeros beyond the last
+      for (int i = 0; i < kScales; ++i) __builtin_memcpy(&scale_held[i], at(i), 16);
+    } else {  // zeros beyond the last
+#pragma unroll
+      for (int i = 0; i < kScales; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int left = blocks - first - e * 4;
           int v = 0;
-          if (left >= 4) __builtin_memcpy(&v, at + e * 4, 4);
+          if (left >= 4) __builtin_memcpy(&v, at(i) + e * 4, 4);
           else
-            for (int k = 0; k < left; ++k) v |= (int)at[e * 4 + k] << (8 * k);
+            for (int k = 0; k < left; ++k) v |= (int)at(i)[e * 4 + k] << (8 * k);
           scale_held[i][e] = v;
         }
-      }
     }
   };
   auto put_scales = [&](int eight) {
