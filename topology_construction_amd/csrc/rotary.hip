@@ -17,10 +17,13 @@ namespace {
 constexpr int kMostThreads = 512;
 constexpr int kTableBytes = 32 << 10;  // of sines and cosines in a workgroup
 
-// cos and sin of p * f radians.
+// cos and sin of p * f radians. The compiler may not fuse operations by itself here: `whole` less its whole turns has to
+// be of the rounded product, whose rounding is added back once (fused, it came in twice: angles near 2^31 radians were
+// off by 1.8e-7, of 2^51 radians by 0.1).
 __device__ __forceinline__ float2 turn_of(int p, float f) {
+#pragma clang fp contract(off)
   constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi) as a sum
-  const double x = p, hi = (double)f * kHi, lo = fma((double)f, kHi, -hi) + (double)f * kLo;
+  const double x = p, hi = (double)f * kHi, lo = fma((double)f, kLo, fma((double)f, kHi, -hi));
   const double whole = x * hi;
   double t = (whole - rint(whole)) + fma(x, lo, fma(x, hi, -whole));  // turns
   t -= rint(t);
