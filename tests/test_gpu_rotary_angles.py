@@ -43,3 +43,18 @@ def _check(low, high, dtype, interleaved, seed):
 def test_angles(low, high, dtype, interleaved):
     print(f"[angles] {low} to {high} {dtype} interleaved {interleaved}", flush=True)
     _check(low, high, dtype, interleaved, int(high))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("low,high", [(2.0 ** 39, 2.0 ** 41), (2.0 ** 40, 1e18), (1e18, 1e30), (1e30, torch.finfo(torch.float32).max), (1e-45, 1e-30)])
+def test_angles_of_any_finite_frequency(low, high, interleaved):
+    print(f"[angles] {low} to {high} interleaved {interleaved}", flush=True)
+    _check(low, high, torch.float32, interleaved, 5)
+
+
+def test_frequencies_that_are_not_finite():
+    """NaN in their own pairs, and in no other."""
+    freqs = torch.tensor([1.0, math.inf, -math.inf, math.nan, 3e38], device="cuda")
+    at = torch.tensor([[0], [3], [-2 ** 31]], dtype=torch.int32, device="cuda")
+    out = binding.tc_rotary(torch.ones(3, 10, device="cuda"), at, freqs)
+    assert out.isnan().tolist() == [[False, True, True, True, False] * 2] * 3

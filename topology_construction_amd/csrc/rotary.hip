@@ -3,9 +3,9 @@
 //
 //   (x1, x2) -> (x1 cos - x2 sin, x1 sin + x2 cos)
 //
-// The inverse, by the opposite angle, is also the gradient. Coordinates are any 32-bit integers, so an angle can
-// be 2^31 radians: it is reduced in 64 bits, in turns, where subtracting whole turns is exact. Memory bounds
-// it: a workgroup puts the sines of its rows into LDS once, for all heads, while its rows are under way.
+// The inverse, by the opposite angle, is also the gradient. Coordinates are any 32-bit integers and frequencies any finite
+// ones, so an angle can be 2^159 radians: it is reduced in 64 bits, in turns, where subtracting whole turns is exact. Memory
+// bounds it: a workgroup puts the sines of its rows into LDS once, for all heads, while its rows are under way.
 #include <type_traits>
 
 #include "rows.hpp"
@@ -17,14 +17,35 @@ namespace {
 constexpr int kMostThreads = 512;
 constexpr int kTableBytes = 32 << 10;  // of sines and cosines in a workgroup
 
+// The first 224 bits of 1 / (2 pi).
+__constant__ const uint32_t kTurnBits[7] = {0x28be60db, 0x9391054a, 0x7f09d5f4, 0x7d4d3770, 0x36d8a566, 0x4f10e410, 0x7f9458ea};
+
+// f radians in turns, less whole ones, as hi + lo to 2^-64, for |f| from 2^40 on, by the method of Payne and Hanek: f is
+// m 2^e, and of 1 / (2 pi) the bits before number e make whole turns. NaN for what is not finite.
+__device__ __forceinline__ void turns_far(float f, double& hi, double& lo) {
+  const uint32_t bits = __float_as_uint(f), m = (bits & 0x7fffff) | 0x800000;
+  const int e = min((int)(bits >> 23 & 255) - 150, 104), last = (e + 31) >> 5;  // 17 to 104; the word that holds bit e, or the next
+  auto word = [&](int i) { return __builtin_amdgcn_alignbit(kTurnBits[last - 1 + i], kTurnBits[last + i], 32 * last - e); };
+  const uint64_t turns = ((uint64_t)m * word(2) >> 32) + (uint64_t)m * word(1) + ((uint64_t)(m * word(0)) << 32);
+  const float sign = copysignf(1.0f, f) + (f - f);
+  hi = (double)(int32_t)(turns >> 32) * 0x1p-32 * sign;
+  lo = (double)(uint32_t)turns * 0x1p-64 * sign;
+}
+
 // cos and sin of p * f radians. The compiler may not fuse operations by itself here: `whole` less its whole turns has to
 // be of the rounded product, whose rounding is added back once (fused, it came in twice: angles near 2^31 radians were
 // off by 1.8e-7, of 2^51 radians by 0.1).
 __device__ __forceinline__ float2 turn_of(int p, float f) {
 #pragma clang fp contract(off)
-  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi) as a sum
-  const double x = p, hi = (double)f * kHi, lo = fma((double)f, kLo, fma((double)f, kHi, -hi));
-  const double whole = x * hi;
+  double hi, lo;  // f in turns
+  if (fabsf(f) < 0x1p40f) {
+    constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;  // 1 / (2 pi) as a sum, to 2^-110
+    hi = (double)f * kHi;
+    lo = fma((double)f, kLo, fma((double)f, kHi, -hi));
+  } else {
+    turns_far(f, hi, lo);
+  }
+  const double x = p, whole = x * hi;
   double t = (whole - rint(whole)) + fma(x, lo, fma(x, hi, -whole));  // turns
   t -= rint(t);
   const double quarter = rint(4.0 * t);
