@@ -8,6 +8,7 @@
 #include <ATen/EmptyTensor.h>
 #include <ATen/MemoryOverlap.h>
 #include <c10/core/GradMode.h>
+#include <c10/core/impl/LocalDispatchKeySet.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -88,10 +89,15 @@ void* vector(const Tensor& t, const char* name, at::ScalarType dtype, int device
 }
 
 // An output on the current device, which `like` is on. torch's dispatcher takes a third of a microsecond for each, so its own
-// allocator is asked directly; which one that is, the first output tells.
+// allocator is asked directly, but where a mode answers for the dispatcher (one of fake tensors, or one that watches). Which
+// allocator that is, the first output that the dispatcher makes by itself tells.
 Tensor empty(const Tensor& like, at::IntArrayRef shape, at::ScalarType dtype) {
-  static c10::Allocator* const allocator =
-      at::empty({1}, like.options().requires_grad(false).memory_format(at::MemoryFormat::Contiguous)).storage().allocator();
+  auto ask = [&](at::IntArrayRef shape) {
+    return at::empty(shape, like.options().dtype(dtype).requires_grad(false).memory_format(at::MemoryFormat::Contiguous));
+  };
+  const auto answers = c10::impl::tls_local_dispatch_key_set().included_ - c10::default_included_set;
+  if (!answers.empty()) return ask(shape);
+  static c10::Allocator* const allocator = ask({1}).storage().allocator();
   return at::detail::empty_generic(shape, allocator, c10::DispatchKeySet(c10::DispatchKey::CUDA), dtype,
                                    at::MemoryFormat::Contiguous);
 }
