@@ -493,7 +493,9 @@ int64_t tc_layer_norm_backward_workspace(int64_t n_rows, int32_t channels);
  *   interleaved  1: pair i is channels 2 i and 2 i + 1; 0: channels i and pairs + i.
  *                Channels from 2 * pairs on are copied.
  *   d_out        dtype[n_rows][heads][dim] with its own strides; rows and heads may not overlap
- *                one another. It may be d_x itself, with the same strides. */
+ *                one another. It may be d_x itself, with the same strides, or else share no element with it
+ *                (other parts of the same rows, heads or rows between its own). An overlap is refused, and so are
+ *                different strides of the two that interleave more than 2^18 times. */
 tc_status tc_rotary(const void* d_x, int64_t x_row_stride, int64_t x_head_stride, int64_t n_rows, int32_t heads,
                     int32_t dim, int32_t dtype, const int32_t* d_positions, int64_t position_stride, int32_t n_axes,
                     const int32_t* h_sections, const float* d_freqs, int32_t interleaved, int32_t inverse, void* d_out,

@@ -755,7 +755,8 @@ def tc_rotary(x, positions, freqs, sections=None, interleaved: bool = False, inv
     positions[row, axis] * freqs[pair] radians. positions int32 [rows, axes], 1 to 4 axes (a batch's tc_enumerate_ijk, or a
     token's time, height and width); `sections` says how many pairs each axis turns, freqs float32 [pairs] by
     how much a step. Pair i is channels i and pairs + i, or `interleaved` 2 i and 2 i + 1; channels from 2 * pairs on are
-    copied. `inverse` turns back. The result is a new tensor, or goes into `out` (which may be x). Where autograd
+    copied. `inverse` turns back. The result is a new tensor, or goes into `out`, which may be x, or another part of the same
+    memory (a packed row's other heads) that shares no element with x: an overlap is refused. Where autograd
     records, x may require a gradient (`out` is refused then), positions and freqs may not."""
     ops = _ops()
     if ops.records(freqs):

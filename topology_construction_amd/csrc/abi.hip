@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "internal.hpp"
+#include "overlap.hpp"
 
 namespace {
 
@@ -1050,16 +1051,20 @@ tc_status tc_rotary(const void* d_x, int64_t x_row_stride, int64_t x_head_stride
     need(inverse == 0 || inverse == 1, "inverse must be 0 or 1");
     check_rows(d_x, x_row_stride, n_rows, "d_x");
     need(x_head_stride >= 0, "d_x: negative head stride");
-    check_rows(d_positions, position_stride, n_rows, "d_positions");
-    need(d_freqs || n_rows == 0, "d_freqs is NULL");
     need(d_out || n_rows == 0, "d_out is NULL");
     need(out_row_stride >= 0 && out_head_stride >= 0, "d_out: negative stride");
+    a.in_place = d_out == d_x && (n_rows < 2 || out_row_stride == x_row_stride) && (heads < 2 || out_head_stride == x_head_stride);
     if (n_rows > 0) {
       // heads inside rows, or rows inside heads
       need(nested(dim, heads, out_head_stride, n_rows, out_row_stride) ||
                nested(dim, n_rows, out_row_stride, heads, out_head_stride),
            "the rows or heads of d_out overlap");
+      need(a.in_place || tc::overlap({d_x, x_row_stride, x_head_stride}, {d_out, out_row_stride, out_head_stride}, n_rows, heads, dim,
+                                     dtype == TC_F32 ? 4 : 2) == tc::Overlap::none,
+           "d_out overlaps d_x without being d_x");
     }
+    check_rows(d_positions, position_stride, n_rows, "d_positions");
+    need(d_freqs || n_rows == 0, "d_freqs is NULL");
     a.x = d_x;
     a.x_row = x_row_stride;
     a.x_head = x_head_stride;
@@ -1076,7 +1081,6 @@ tc_status tc_rotary(const void* d_x, int64_t x_row_stride, int64_t x_head_stride
     a.out = d_out;
     a.out_row = out_row_stride;
     a.out_head = out_head_stride;
-    a.in_place = d_out == d_x && out_row_stride == x_row_stride && out_head_stride == x_head_stride;
     tc::rotary(a, (hipStream_t)stream);
     return TC_OK;
   });

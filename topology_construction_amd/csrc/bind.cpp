@@ -6,7 +6,6 @@
 
 #include <ATen/ATen.h>
 #include <ATen/EmptyTensor.h>
-#include <ATen/MemoryOverlap.h>
 #include <c10/core/GradMode.h>
 #include <c10/core/impl/LocalDispatchKeySet.h>
 #include <torch/csrc/Dtype.h>
@@ -16,6 +15,7 @@
 #include <optional>
 #include <string>
 
+#include "overlap.hpp"
 #include "topo.h"
 
 namespace {
@@ -377,10 +377,10 @@ PyObject* rotary(const Args& g) {
       bad_value("out requires a gradient, which this call has none for");
     if (out.sizes() != x.sizes()) bad_value("out has another shape than x");
     o = heads_of(out, "out", type, device);
-    // x itself, or apart from it (strided parts of one tensor are the caller's to keep apart)
+    // x itself, or apart from it
     const bool same = o.p == h.p && (h.rows < 2 || o.row == h.row) && (h.heads < 2 || o.head == h.head);
     if (x.numel() > 0 && !same &&
-        (o.p == h.p || at::get_overlap_status(x, out) == at::MemOverlapStatus::Partial))
+        tc::overlap({h.p, h.row, h.head}, {o.p, o.row, o.head}, h.rows, h.heads, h.dim, x.element_size()) != tc::Overlap::none)
       bad_value("out overlaps x without being x");
   }
   if (h.heads > 0)
