@@ -1,5 +1,5 @@
-// 8-bit (and packed 4-bit) rows and weights as the matrix instructions take them: loads, tiles and their order
-// in LDS, stores of results (product.hip, conv.hip, product_mx4.hip).
+// 8-bit rows and weights as the matrix instructions take them: loads, tiles and their order in LDS, stores of results
+// (product.hip, conv.hip); packed 4-bit ones share the loads, tiles and waits (mx4.hpp, product_mx4.hip).
 #pragma once
 
 #include "rows.hpp"
@@ -12,8 +12,8 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 // CNT consecutive output channels of one row from n on, rounded to T. Rows on 16-byte
 // boundaries (`wide`) are stored past the caches, which keeps the inputs there
 // (16384 x 4096 -> 4096: 230 for 260 us, 124800 x 256 -> 768: 65 for 106 us, in one run).
-template <typename T, int CNT, typename Args>
-__device__ __forceinline__ void store_run(const Args& a, i64 row, int n, const float v[CNT], bool wide) {
+template <typename T, int CNT>
+__device__ __forceinline__ void store_run(const ProductArgs& a, i64 row, int n, const float v[CNT], bool wide) {
   T* out = static_cast<T*>(a.out) + row * a.out_stride + n;
   T r[CNT];
 #pragma unroll
@@ -96,14 +96,6 @@ __device__ __forceinline__ void tile_place(i64 tile, i64 tiles_m, int tiles_n, i
   tm = first + at % size;
   tn = at / size;
 }
-
-// Row r of the weights' matrix instruction t of a wave's 64 channels, such that a lane's
-// results of two instructions are 8 consecutive channels and the four lanes of an output
-// row store 64 bytes side by side; and the LDS slot key of such a row.
-__device__ __forceinline__ constexpr int w_row(int t, int r) {
-  return (t >> 1) * 32 + (r >> 2) * 8 + (t & 1) * 4 + (r & 3);
-}
-__device__ __forceinline__ int w_key(int row) { return ((row >> 1) & 1) | ((row >> 2) & 2); }
 
 // This wave's LDS reads and writes are done.
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }

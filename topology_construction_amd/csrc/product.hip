@@ -11,6 +11,14 @@ namespace {
 
 // ------------------------------------------------------------------ plain product, many tiles
 
+// Row r of the weights' matrix instruction t of a wave's 64 channels, such that a lane's
+// results of two instructions are 8 consecutive channels and the four lanes of an output
+// row store 64 bytes side by side; and the LDS slot key of such a row.
+__device__ __forceinline__ constexpr int w_row(int t, int r) {
+  return (t >> 1) * 32 + (r >> 2) * 8 + (t & 1) * 4 + (r & 3);
+}
+__device__ __forceinline__ int w_key(int row) { return ((row >> 1) & 1) | ((row >> 2) & 2); }
+
 // BM x BN outputs per workgroup, (BM / WM) * (BN / 64) waves of WM x 64 each, in
 // steps of 64 input channels. kDirect: rows and chunks on 16-byte boundaries go
 // straight into LDS, kBufs - 1 steps ahead of the products, or (kPer = 2, four buffers)
