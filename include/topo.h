@@ -458,7 +458,8 @@ tc_status tc_layer_norm(const void* d_x, int64_t x_stride, const void* d_residua
  *   grad_x = s (g - mean(g) - u mean(g u)) + dh, rounded to dtype: the gradient of x, and of r alike;
  *   grad_weight = sum over rows of dy u, grad_bias = sum over rows of dy: 32-bit float sums in an order
  *   that only n_rows, channels and dtype decide.
- * m is h's mean as the row has it; d_mean, its rounding to 32 bits, is where the sums start from.
+ * m is h's mean as the row has it; d_mean, its rounding to 32 bits, is where the sums start from. A row whose s is
+ * infinite (a spread below 2^-128 with eps = 0) makes its grad_x and all of grad_weight NaN.
  *   d_grad_out    dtype[n_rows][channels], grad_out_stride.
  *   d_grad_sum    dh, dtype[n_rows][channels], grad_sum_stride, or NULL (zeros).
  *   d_h           h as tc_layer_norm left it (x where there is no residual), h_stride.

@@ -462,7 +462,7 @@ void launch_tile(const ProductMx4Args& a, hipStream_t s) {
 //   16 x 4096 -> 4096                              9.6                                   7.0    5.5
 //   1 x 1024 -> 4096                               4.0                                          3.4
 // The largest tile that gives most CUs one is best; with no more than two steps of input channels the stores are most of the
-// time, and tiles that leave room for three workgroups a CU hide them.
+// time, and two workgroups of eight waves a CU (62 KB of LDS and 112 registers each) have one's under the other's loads.
 template <typename T>
 void product(const ProductMx4Args& a, hipStream_t s) {
   const i64 cus = device_cu_count();
