@@ -58,7 +58,7 @@ __device__ __forceinline__ float2 turn_of(int p, float f) {
 // which go one by one. A thread has the same unit of kDepth rows, all asked for before the sines are made.
 //
 // kWide: outputs on 16-byte boundaries, of which a wave has whole lines, go past the caches: 60000 x 8 x 128 bf16
-// 38 for 53 us, neighbours 40 for 56; 124800 x 16 x 64, neighbours, 110 for 120 (4.7 TB/s). Halves of 64 bytes
+// 42 for 53 us, neighbours 38 for 56; 124800 x 16 x 64, neighbours, 110 for 120 (4.7 TB/s). Halves of 64 bytes
 // (124800 x 16 x 64) would take 130 for 115 that way.
 template <typename T, bool kNeighbours, bool kWide>
 struct UnitOf {
